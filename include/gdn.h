@@ -347,6 +347,145 @@ GDN_API gdn_status gdn_kda_decode(const gdn_config *cfg, const gdn_kda_params *p
                                   void *y, void *stream);
 
 /*
+ * Selective state-space (SSM) mixer: a scan with one scalar decay per head and
+ * token, behind the same kernel-4 causal convolution (the state-space dual
+ * form of Dao and Gu, "Transformers are SSMs", 2024).  The pages have no
+ * counterpart; it is the third linear-recurrence mixer beside GDN and KDA and
+ * keeps their conventions: packed varlen prompts, a resident float32 state
+ * [P][S] per head, a conv window, single-token decode in place.  Per token:
+ *     x | B | C = SiLU(conv_w * xbc + conv_b)       (H P | G S | G S channels)
+ *     delta = min(max(softplus(dt + dt_bias), dt_min), dt_max)      per head
+ *     S_t = exp(-exp(A_log) delta) S_{t-1} + delta x_t B_t^T
+ *     y_t = (S_t C_t + D x_t) * SiLU(z_t)
+ * where head h reads B and C of group h / (H / G).  All arithmetic between the
+ * inputs and y is carried in float32 (matrix products on the tensor cores take
+ * each operand as a sum of two bfloat16 parts, three products each, which
+ * keeps about 16 bits of every operand).
+ *
+ * Row strides: xbc, dt and z may be parts of wider rows (one in-projection's
+ * output): the stride is in elements, at least the part's own length, and for
+ * xbc and z a multiple of 16 bytes.  Every other tensor is contiguous.
+ */
+typedef struct gdn_ssm_config {
+    int32_t num_groups;  /* G >= 1: groups of heads that share B and C */
+    int32_t num_heads;   /* H, a multiple of G */
+    int32_t head_dim;    /* P: 64 or 128 */
+    int32_t state_dim;   /* S: 64 or 128 */
+    int32_t conv_kernel; /* causal conv width; the library supports 4 */
+    float dt_min;        /* clamp of delta: 0 <= dt_min <= dt_max; dt_max may be +infinity */
+    float dt_max;
+    int32_t act_dtype;   /* gdn_dtype of xbc, dt, z, y and the conv windows */
+    int32_t segments;    /* prefill: segments per sequence, 0 = the library's choice, else 1..16 */
+} gdn_ssm_config;
+
+typedef struct gdn_ssm_params { /* float32 device arrays */
+    const float *conv_w;  /* [H P + 2 G S, conv_kernel]; tap conv_kernel-1 multiplies the current token */
+    const float *conv_b;  /* [H P + 2 G S], or NULL for none */
+    const float *A_log;   /* [H] */
+    const float *dt_bias; /* [H], or NULL for none */
+    const float *D;       /* [H], or NULL for none */
+} gdn_ssm_params;
+
+/*
+ * Workspace bytes of gdn_ssm_prefill for `total_tokens` packed tokens in
+ * `batch` sequences (0 when total_tokens is 0); errors as
+ * gdn_prefill_workspace_size.
+ */
+GDN_API gdn_status gdn_ssm_prefill_workspace_size(const gdn_ssm_config *cfg, int32_t batch,
+                                                  int64_t total_tokens, size_t *bytes);
+
+/*
+ * Prefill over a packed varlen batch; cu_seqlens, windows and workspace rules
+ * as in gdn_prefill.
+ *   xbc           [N, H P + 2 G S]  act_dtype, rows xbc_stride apart: pre-conv x | B | C
+ *   dt            [N, H]            act_dtype, rows dt_stride apart (element aligned)
+ *   z             [N, H, P]         act_dtype, rows z_stride apart, or NULL for no gate
+ *   initial_state [batch, H, P, S]  float32, or NULL for zeros
+ *   initial_conv  [batch, 3, H P + 2 G S] act_dtype, or NULL for zeros
+ *   y             [N, H, P]         act_dtype
+ *   final_state   [batch, H, P, S]  float32, or NULL; may equal initial_state
+ *   final_conv    [batch, 3, H P + 2 G S] act_dtype, or NULL; may equal initial_conv
+ * Rows at and behind cu_seqlens[batch] are left as they were.
+ */
+GDN_API gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *params,
+                                   const void *xbc, int64_t xbc_stride, const void *dt,
+                                   int64_t dt_stride, const void *z, int64_t z_stride,
+                                   const int32_t *cu_seqlens, int32_t batch, int64_t total_tokens,
+                                   const float *initial_state, const void *initial_conv, void *y,
+                                   float *final_state, void *final_conv, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/*
+ * Decode: one token for each of `batch` sequences; state [batch, H, P, S] and
+ * conv_cache [batch, 3, H P + 2 G S] advance in place.  xbc, dt and z as in
+ * gdn_ssm_prefill with one row per sequence.  Needs no workspace.
+ */
+GDN_API gdn_status gdn_ssm_decode(const gdn_ssm_config *cfg, const gdn_ssm_params *params,
+                                  const void *xbc, int64_t xbc_stride, const void *dt,
+                                  int64_t dt_stride, const void *z, int64_t z_stride, float *state,
+                                  void *conv_cache, int32_t batch, void *y, void *stream);
+
+/*
+ * Root-mean-square norm of the residual stream with its addition and an 8-bit
+ * output, the input of gdn_matmul_fp8:
+ *     r = x + residual                         (residual NULL: r = x)
+ *     v = r / sqrt(mean(r^2) + eps) * (weight_offset + weight)
+ *     scale[row][k] = max(max |v[128 k .. 128 k + 127]| / 448, 2^-126)
+ *     q = e4m3(v / scale), rounded to nearest even
+ * The mean runs over dim / groups consecutive elements (groups > 1: the norm
+ * by groups that a state-space mixer's output takes).  With weight = NULL the
+ * norm is left out and v = r: the plain quantisation of, for instance, a
+ * mixer's y before its out-projection.  The sum, the mean and v are float32;
+ * r is not rounded before the norm.  weight_offset 1 gives zero-centred gains
+ * ("Qwen3.8-2.4T-A95B vs Inkling", component table, residual-stream row).
+ * A block that holds a NaN, or an infinity, has that as its scale, and its
+ * elements come back as NaN or zero times that scale.
+ *
+ *   x        [rows, dim]  act_dtype, rows x_stride elements apart (a multiple of 16 bytes)
+ *   residual [rows, dim]  act_dtype, contiguous, or NULL
+ *   weight   [dim]        float32, or NULL
+ *   residual_out [rows, dim] act_dtype: r, or NULL to skip; may equal residual, or x where
+ *                         that is contiguous
+ *   y        [rows, dim]  act_dtype: v, or NULL to skip
+ *   q        [rows, dim]  e4m3 bytes, or NULL to skip (scale then NULL too)
+ *   scale    [rows, ceil(dim / 128)] float32
+ * dim: a positive multiple of 8; with groups > 1, dim / groups a multiple of
+ * 128.  rows = 0 does nothing.
+ */
+typedef struct gdn_norm_config {
+    int64_t rows;
+    int32_t dim;
+    int32_t groups;      /* >= 1, divides dim */
+    float eps;           /* >= 0 */
+    float weight_offset; /* finite */
+    int32_t act_dtype;
+} gdn_norm_config;
+
+GDN_API gdn_status gdn_rmsnorm_fp8(const gdn_norm_config *cfg, const void *x, int64_t x_stride,
+                                   const void *residual, const float *weight, void *residual_out,
+                                   void *y, void *q, float *scale, void *stream);
+
+/*
+ * Matrix product of 8-bit operands with a scale for each block of 128, the
+ * in- and out-projections around a mixer:
+ *     out[m][n] = sum_b a_scale[m][b] w_scale[n / 128][b]
+ *                 sum_{128 b <= k < min(K, 128 b + 128)} a[m][k] w[n][k]
+ *   a        [M, K]  e4m3 bytes            a_scale [M, ceil(K / 128)] float32
+ *   w        [N, K]  e4m3 bytes            w_scale [ceil(N / 128), ceil(K / 128)] float32
+ *   out      [M, N]  out_dtype (a gdn_dtype), rows out_stride elements apart
+ * The products within a block are summed by the tensor core in float32, the
+ * blocks in float32 registers.  K: a positive multiple of 16.  M, N and the
+ * alignment of out's rows are free (out itself is 16-byte aligned, the scales
+ * 4-byte).  Workspace: gdn_matmul_fp8_workspace_size bytes, 16-byte aligned
+ * (0 for most shapes); calls that may overlap on the GPU need one each.
+ */
+GDN_API gdn_status gdn_matmul_fp8_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
+GDN_API gdn_status gdn_matmul_fp8(const void *a, const float *a_scale, const void *w,
+                                  const float *w_scale, int64_t M, int64_t N, int64_t K, void *out,
+                                  int64_t out_stride, int32_t out_dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
  * Size of the fixed device scratch array used by gdn_prefill_noalloc:
  * 64 MiB, held on every GPU that loads the library until the process exits.
  */

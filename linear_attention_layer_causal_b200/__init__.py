@@ -13,6 +13,10 @@ into the library without the built extension raises.
                       initial_state=S0, return_final_state=True)
     y = gdn.decode(cfg, qkv1, a1, b1, z1, state, conv_cache, conv_w, A_log, dt_bias, norm_w)
 
+Beside it: the selective state-space mixer (ssm_prefill, ssm_decode), and what feeds and
+drains a mixer in 8 bits, the residual norm (rmsnorm_fp8, quantize_fp8) and the block-scaled
+product (matmul_fp8).
+
 The layer: kernel-4 causal conv + SiLU over q|k|v, q/k L2 norm, gates
 g = -exp(A_log) softplus(a + dt_bias) and beta = sigmoid(b), the gated delta
 rule on an FP32 state per value head, and the per-head RMSNorm gated by
@@ -24,6 +28,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import cached_property
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -36,7 +41,9 @@ EXPORTED = ("gdn_prefill_workspace_size", "gdn_prefill_segments", "gdn_prefill",
             "gdn_abi_version", "gdn_profile_next_call", "gdn_prefill_noalloc",
             "gdn_prefill_status", "gdn_prefill_noalloc_status", "gdn_wait_limit_next_call",
             "gdn_decode_multi", "gdn_decode_verify", "gdn_decode_commit",
-            "gdn_kda_prefill_workspace_size", "gdn_kda_prefill", "gdn_kda_decode")
+            "gdn_kda_prefill_workspace_size", "gdn_kda_prefill", "gdn_kda_decode",
+            "gdn_ssm_prefill_workspace_size", "gdn_ssm_prefill", "gdn_ssm_decode",
+            "gdn_rmsnorm_fp8", "gdn_matmul_fp8_workspace_size", "gdn_matmul_fp8")
 
 # Fixed scratch of gdn_prefill_noalloc (GDN_NOALLOC_SCRATCH_BYTES in include/gdn.h).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -59,6 +66,25 @@ class _Config(ctypes.Structure):
 class _KdaParams(ctypes.Structure):
     _fields_ = [("conv_w", ctypes.c_void_p), ("A_log", ctypes.c_void_p),
                 ("norm_w", ctypes.c_void_p)]
+
+
+class _SsmConfig(ctypes.Structure):
+    _fields_ = [("num_groups", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("state_dim", ctypes.c_int32),
+                ("conv_kernel", ctypes.c_int32), ("dt_min", ctypes.c_float),
+                ("dt_max", ctypes.c_float), ("act_dtype", ctypes.c_int32),
+                ("segments", ctypes.c_int32)]
+
+
+class _SsmParams(ctypes.Structure):
+    _fields_ = [("conv_w", ctypes.c_void_p), ("conv_b", ctypes.c_void_p),
+                ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("D", ctypes.c_void_p)]
+
+
+class _NormConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("act_dtype", ctypes.c_int32)]
 
 
 class _Params(ctypes.Structure):
@@ -136,6 +162,21 @@ def lib() -> ctypes.CDLL:
         L.gdn_kda_prefill.restype = ctypes.c_int
         L.gdn_kda_decode.argtypes = [cfgp, kpp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
         L.gdn_kda_decode.restype = ctypes.c_int
+        sp, spp = ctypes.POINTER(_SsmConfig), ctypes.POINTER(_SsmParams)
+        L.gdn_ssm_prefill_workspace_size.argtypes = [sp, i32, i64, ctypes.POINTER(sz)]
+        L.gdn_ssm_prefill_workspace_size.restype = ctypes.c_int
+        L.gdn_ssm_prefill.argtypes = [sp, spp, vp, i64, vp, i64, vp, i64, vp, i32, i64, vp, vp, vp,
+                                      vp, vp, vp, sz, vp]
+        L.gdn_ssm_prefill.restype = ctypes.c_int
+        L.gdn_ssm_decode.argtypes = [sp, spp, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, vp]
+        L.gdn_ssm_decode.restype = ctypes.c_int
+        L.gdn_rmsnorm_fp8.argtypes = [ctypes.POINTER(_NormConfig), vp, i64, vp, vp, vp, vp, vp, vp,
+                                      vp]
+        L.gdn_rmsnorm_fp8.restype = ctypes.c_int
+        L.gdn_matmul_fp8_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+        L.gdn_matmul_fp8_workspace_size.restype = ctypes.c_int
+        L.gdn_matmul_fp8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i64, i32, vp, sz, vp]
+        L.gdn_matmul_fp8.restype = ctypes.c_int
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_profile_next_call.argtypes = [vp, vp]
@@ -448,3 +489,283 @@ def kda_decode(cfg: Config, qkv, zdec, b, gate, state, conv_cache, conv_w, A_log
     if st != GDN_OK:
         raise GdnError(st, "gdn_kda_decode")
     return y
+
+
+# ------------------------------------------------------ selective state-space mixer
+
+
+@dataclass(frozen=True)
+class SsmConfig:
+    """Head layout of one selective state-space mixer: H heads of P channels in G groups
+    that share B and C, and S state columns (see gdn_ssm_config in include/gdn.h)."""
+    num_groups: int
+    num_heads: int
+    head_dim: int
+    state_dim: int
+    conv_kernel: int = 4
+    dt_min: float = 0.0
+    dt_max: float = float("inf")
+    act_dtype: str = "bf16"  # "bf16" or "f32"
+    segments: int = 0        # prefill: segments per sequence (0 = the library's choice)
+
+    @property
+    def conv_dim(self) -> int:
+        return self.num_heads * self.head_dim + 2 * self.num_groups * self.state_dim
+
+    @cached_property
+    def _struct(self) -> _SsmConfig:
+        return _SsmConfig(self.num_groups, self.num_heads, self.head_dim, self.state_dim,
+                          self.conv_kernel, self.dt_min, self.dt_max,
+                          GDN_BF16 if self.act_dtype == "bf16" else GDN_F32, self.segments)
+
+    def _c(self) -> _SsmConfig:
+        return self._struct
+
+
+def _check(name, t, shape, dtype, device, optional=True):
+    """Address of contiguous tensor `t` of this shape, type and device (None where optional)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dtype, device, optional=False):
+    """As _check, but rows (dimension 0) may be apart: (address, row stride in elements)."""
+    if t is None:
+        if optional:
+            return None, 0
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    strides, n = t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if strides[i] != n and shape[i] != 1:
+            raise ValueError(f"the rows of {name} must be contiguous, got strides {strides}")
+        n *= shape[i]
+    return t.data_ptr(), strides[0] if shape[0] > 1 else n
+
+
+class _on:
+    """Makes the tensors' device current and gives the stream to launch on: that device's current
+    one, or the caller's, which then also owns what is allocated inside (a temporary workspace must
+    not return to another stream's pool while a kernel uses it)."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError("tensors passed to the library must live on a CUDA device")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self.guard = None
+        if stream is not None:
+            self.guard = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+            stream = torch.cuda.current_stream(device)
+        else:
+            stream = torch.cuda.current_stream()
+        self.stream = stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _workspace(workspace, need, device):
+    """(address, bytes) of the caller's workspace or of a new one, and the tensor to keep alive."""
+    import torch
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def ssm_prefill_workspace_size(cfg: SsmConfig, batch: int, total_tokens: int) -> int:
+    n = ctypes.c_size_t(0)
+    st = lib().gdn_ssm_prefill_workspace_size(ctypes.byref(cfg._c()), batch, total_tokens,
+                                              ctypes.byref(n))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_ssm_prefill_workspace_size")
+    return n.value
+
+
+def _ssm_params(cfg, dev, conv_w, conv_b, A_log, dt_bias, D):
+    import torch
+    f32, C, H = torch.float32, cfg.conv_dim, cfg.num_heads
+    return _SsmParams(_check("conv_w", conv_w, (C, cfg.conv_kernel), f32, dev, False),
+                      _check("conv_b", conv_b, (C,), f32, dev),
+                      _check("A_log", A_log, (H,), f32, dev, False),
+                      _check("dt_bias", dt_bias, (H,), f32, dev), _check("D", D, (H,), f32, dev))
+
+
+def ssm_prefill(cfg: SsmConfig, xbc, dt, cu_seqlens, conv_w, A_log, *, conv_b=None, dt_bias=None,
+                D=None, z=None, initial_state=None, initial_conv=None, return_final_state=False,
+                return_final_conv=False, y=None, final_state=None, final_conv=None,
+                workspace=None, stream=None) -> dict:
+    """Packed varlen prefill of the selective state-space mixer (gdn_ssm_prefill).
+
+    xbc [N, H P + 2 G S], dt [N, H] and z [N, H, P] may be slices of wider rows.  Returns a dict
+    with "y" [N, H, P] and, when requested or passed in, "final_state" [B, H, P, S] float32 and
+    "final_conv" [B, 3, H P + 2 G S]; ``final_state`` may be ``initial_state``."""
+    import torch
+    N, B, dev, act = xbc.shape[0], cu_seqlens.shape[0] - 1, xbc.device, _act(cfg)
+    H, P, S, C = cfg.num_heads, cfg.head_dim, cfg.state_dim, cfg.conv_dim
+    with _on(dev, stream) as s:
+        xp, xs = _rows("xbc", xbc, (N, C), act, dev)
+        dp, ds = _rows("dt", dt, (N, H), act, dev)
+        zp, zs = _rows("z", z, (N, H, P), act, dev, optional=True)
+        need = ssm_prefill_workspace_size(cfg, B, N)
+        if y is None:
+            y = torch.empty((N, H, P), dtype=act, device=dev)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((B, H, P, S), dtype=torch.float32, device=dev)
+        if final_conv is None and return_final_conv:
+            final_conv = torch.empty((B, cfg.conv_kernel - 1, C), dtype=act, device=dev)
+        wp, wb, keep = _workspace(workspace, need, dev)
+        state, window = (B, H, P, S), (B, cfg.conv_kernel - 1, C)
+        st = lib().gdn_ssm_prefill(
+            ctypes.byref(cfg._c()), ctypes.byref(_ssm_params(cfg, dev, conv_w, conv_b, A_log, dt_bias, D)),
+            xp, xs, dp, ds, zp, zs, _check("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, dev, False),
+            B, N, _check("initial_state", initial_state, state, torch.float32, dev),
+            _check("initial_conv", initial_conv, window, act, dev), _check("y", y, (N, H, P), act, dev),
+            _check("final_state", final_state, state, torch.float32, dev),
+            _check("final_conv", final_conv, window, act, dev), wp, wb, s)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_ssm_prefill")
+    out = {"y": y}
+    if final_state is not None:
+        out["final_state"] = final_state
+    if final_conv is not None:
+        out["final_conv"] = final_conv
+    return out
+
+
+def ssm_decode(cfg: SsmConfig, xbc, dt, state, conv_cache, conv_w, A_log, *, conv_b=None,
+               dt_bias=None, D=None, z=None, y=None, stream=None):
+    """One token per sequence (gdn_ssm_decode); `state` and `conv_cache` are updated in place.
+    Returns y [B, H, P]."""
+    import torch
+    B, dev, act = xbc.shape[0], xbc.device, _act(cfg)
+    H, P, S, C = cfg.num_heads, cfg.head_dim, cfg.state_dim, cfg.conv_dim
+    with _on(dev, stream) as s:
+        xp, xs = _rows("xbc", xbc, (B, C), act, dev)
+        dp, ds = _rows("dt", dt, (B, H), act, dev)
+        zp, zs = _rows("z", z, (B, H, P), act, dev, optional=True)
+        if y is None:
+            y = torch.empty((B, H, P), dtype=act, device=dev)
+        st = lib().gdn_ssm_decode(
+            ctypes.byref(cfg._c()), ctypes.byref(_ssm_params(cfg, dev, conv_w, conv_b, A_log, dt_bias, D)),
+            xp, xs, dp, ds, zp, zs, _check("state", state, (B, H, P, S), torch.float32, dev, False),
+            _check("conv_cache", conv_cache, (B, cfg.conv_kernel - 1, C), act, dev, False), B,
+            _check("y", y, (B, H, P), act, dev), s)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_ssm_decode")
+    return y
+
+
+# ----------------------------------------------- norm and projections in 8 bits
+
+BLOCK = 128  # elements that share a scale
+
+
+def _norm_call(x, weight, residual, groups, eps, weight_offset, q, scale, residual_out, y, want_r,
+               want_y, stream):
+    import torch
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x must be bfloat16 or float32 [rows, dim], got {x.dtype} {tuple(x.shape)}")
+    shape, dev, act = x.shape, x.device, x.dtype
+    rows, dim = shape
+    blocks = (rows, -(-dim // BLOCK))
+    with _on(dev, stream) as s:
+        xp, xs = _rows("x", x, shape, act, dev)
+        if q is None:
+            q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        if scale is None:
+            scale = torch.empty(blocks, dtype=torch.float32, device=dev)
+        if residual_out is None and want_r:
+            residual_out = torch.empty(shape, dtype=act, device=dev)
+        if y is None and want_y:
+            y = torch.empty(shape, dtype=act, device=dev)
+        cfg = _NormConfig(rows, dim, groups, eps, weight_offset, GDN_BF16 if act == torch.bfloat16 else GDN_F32)
+        st = lib().gdn_rmsnorm_fp8(
+            ctypes.byref(cfg), xp, xs, _check("residual", residual, shape, act, dev),
+            _check("weight", weight, (dim,), torch.float32, dev),
+            _check("residual_out", residual_out, shape, act, dev), _check("y", y, shape, act, dev),
+            _check("q", q, shape, torch.float8_e4m3fn, dev),
+            _check("scale", scale, blocks, torch.float32, dev), s)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_rmsnorm_fp8")
+    return q, scale, residual_out, y
+
+
+def rmsnorm_fp8(x, weight, *, residual=None, groups=1, eps=1e-6, weight_offset=0.0, return_y=False,
+                q=None, scale=None, residual_out=None, y=None, stream=None) -> dict:
+    """RMS norm of x (+ residual) with an e4m3 output and a float32 scale for each 128 elements
+    (gdn_rmsnorm_fp8).  Returns a dict with "q" [rows, dim], "scale" [rows, ceil(dim / 128)] and,
+    with a residual, "residual" = x + residual (written to ``residual_out``, which may be
+    ``residual``); with ``return_y`` also the norm's unquantised output "y"."""
+    if weight is None:
+        raise ValueError("weight is required (quantize_fp8 quantises without a norm)")
+    q, scale, residual_out, y = _norm_call(x, weight, residual, groups, eps, weight_offset, q, scale,
+                                           residual_out, y, residual is not None, return_y, stream)
+    out = {"q": q, "scale": scale}
+    if residual_out is not None:
+        out["residual"] = residual_out
+    if y is not None:
+        out["y"] = y
+    return out
+
+
+def quantize_fp8(x, *, q=None, scale=None, stream=None):
+    """x [rows, dim] as e4m3 with a float32 scale for each 128 elements of a row: (q, scale)."""
+    return _norm_call(x, None, None, 1, 0.0, 0.0, q, scale, None, None, False, False, stream)[:2]
+
+
+def matmul_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    st = lib().gdn_matmul_fp8_workspace_size(M, N, K, ctypes.byref(n))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_matmul_fp8_workspace_size")
+    return n.value
+
+
+def matmul_fp8(a, a_scale, w, w_scale, *, out_dtype=None, out=None, workspace=None, stream=None):
+    """a [M, K] times w [N, K] transposed, both e4m3 with scales for blocks of 128 (1 x 128 of a,
+    128 x 128 of w; gdn_matmul_fp8).  Returns out [M, N] in ``out_dtype`` (bfloat16, the default,
+    or float32); a given ``out`` may have rows apart."""
+    import torch
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a must be [M, K] and w [N, K]")
+    (M, K), N, dev = a.shape, w.shape[0], a.device
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    kb, f8 = -(-K // BLOCK), torch.float8_e4m3fn
+    with _on(dev, stream) as s:
+        ap, wp = _check("a", a, (M, K), f8, dev), _check("w", w, (N, K), f8, dev)
+        sa = _check("a_scale", a_scale, (M, kb), torch.float32, dev, False)
+        sw = _check("w_scale", w_scale, (-(-N // BLOCK), kb), torch.float32, dev, False)
+        wsp, wsb, keep = _workspace(workspace, matmul_fp8_workspace_size(M, N, K), dev)
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        op, os_ = _rows("out", out, (M, N), out_dtype, dev)
+        st = lib().gdn_matmul_fp8(ap, sa, wp, sw, M, N, K, op, os_,
+                                  GDN_BF16 if out_dtype == torch.bfloat16 else GDN_F32, wsp, wsb, s)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_matmul_fp8")
+    return out

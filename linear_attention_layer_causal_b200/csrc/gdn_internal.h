@@ -134,4 +134,55 @@ cudaError_t launch_kda_prefill(const PrefillArgs &p, cudaStream_t s);
 cudaError_t launch_kda_decode(const DecodeArgs &p, cudaStream_t s);
 size_t decode_multi_smem_bytes(int G, int D, int k, int mode);
 
+// Selective state-space mixer: prefill and decode (decode: N = batch, state = init_state).
+struct SsmArgs {
+    int H, G, P, S;          // heads, groups, head dim, state dim
+    bool bf16;
+    float dt_min, dt_max;
+    const void *xbc, *dt, *z;
+    int64_t xbc_stride, dt_stride, z_stride; // elements
+    const int32_t *cu = nullptr;
+    int batch;
+    int64_t N;
+    const float *init_state = nullptr;
+    const void *init_conv = nullptr;
+    void *y;
+    float *final_state = nullptr;
+    void *final_conv = nullptr;
+    float *state = nullptr;      // decode: resident states
+    void *conv_cache = nullptr;  // decode: resident windows
+    const float *conv_w, *conv_b, *A_log, *dt_bias, *D;
+    void *ws = nullptr;
+    constexpr int conv_dim() const { return H * P + 2 * G * S; }
+};
+size_t ssm_workspace_bytes(const gdn_ssm_config *c, int batch, int64_t N);
+cudaError_t launch_ssm_prefill(const SsmArgs &p, cudaEvent_t begin, cudaEvent_t end, cudaStream_t s);
+cudaError_t launch_ssm_decode(const SsmArgs &p, cudaStream_t s);
+
+struct NormArgs {
+    int64_t rows;
+    int dim, groups;
+    bool bf16;
+    float eps, weight_offset;
+    const void *x;
+    int64_t x_stride;
+    const void *residual;
+    const float *weight;
+    void *residual_out, *y, *q;
+    float *scale;
+};
+cudaError_t launch_norm(const NormArgs &p, cudaStream_t s);
+
+struct MatmulArgs {
+    const void *a, *w;
+    const float *a_scale, *w_scale;
+    int64_t M, N, K;
+    void *out;
+    int64_t out_stride;
+    bool out_bf16;
+    void *ws;
+};
+size_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_matmul(const MatmulArgs &p, cudaStream_t s);
+
 } // namespace gdn
