@@ -3,10 +3,12 @@
 //     out[m][n] = sum_b sa[m][b] sw[n / 128][b] sum_{k in block b} a[m][k] w[n][k].
 // The scales change with the block, so the inner sum of every block is finished
 // in the tensor core's accumulator and then added, scaled, to a float32 register
-// sum.  Two kernels:
-//   - wide_kernel (tcgen05, operands by TMA): a 128 x BN tile of out per block.
-//   - narrow_kernel (few rows of a): bound by reading w once; w goes from global
-//     memory straight into the registers of mma.sync.
+// sum.  Both kernels are one loop over blocks of k with five roles: a TMA warp,
+// an MMA warp (tcgen05, e4m3), two warps that stage the scales, and warpgroups
+// that read each finished block from TMEM and add it.
+//   - wide_kernel: 128 rows of a by 256 rows of w, persistent over tiles.
+//   - thin_kernel: 128 rows of w by BN <= 128 rows of a, the k axis split over
+//     a cluster; for few rows of a, where reading w once is the bound.
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
 #include "gdn_sm100.cuh"
@@ -19,7 +21,6 @@ using namespace sm100;
 
 constexpr int kSMs = 148;
 constexpr int kBK = 128;              // k of a stage: one scale block
-constexpr int kABytes = 128 * kBK;    // 128 rows of a
 constexpr uint32_t kStatusTimeout = 1u;
 
 // ------------------------------------------------------------------- wide
@@ -68,34 +69,154 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// float at `addr` of this block's shared memory, read from block `rank` of the cluster
-__device__ __forceinline__ float ld_dsmem(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
-                 "ld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
-    return v;
+// The address in block `rank` of the cluster of this block's shared-memory address.
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_dsmem(uint32_t addr, unsigned long long x, unsigned long long y) {
+    asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(addr), "l"(x), "l"(y) : "memory");
 }
 
-template <int BN> struct Wide {
-    static constexpr int kStages = BN == 256 ? 4 : 6;
-    static constexpr int kStageBytes = kABytes + BN * kBK;
-    static constexpr int kGroups = BN / 128;           // epilogue warpgroups
-    static constexpr int kThreads = 128 + 128 * kGroups;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes;
+// Scales of four blocks of k at a time, staged in shared memory by two warps.
+constexpr int kScaleSlots = 4;
+
+// Barriers and roles shared by the two kernels.  A wait that runs out (about a
+// second) makes every role stop at its next wait; what is in flight is waited
+// for before the block ends, and the status word says so.
+struct Waiter {
+    volatile uint32_t *abort_flag;
+    uint32_t *status;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (mbar_try_wait_spin(bar, parity))
+            return true;
+        if (!*abort_flag && mbar_wait_bounded(bar, parity, kDefaultWaitLimit))
+            return true;
+        *abort_flag = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
+    }
 };
 
-// 128 columns of one row from registers to out.
+// Position in a ring of N slots and the parity of its current round.
+template <int N> struct Ring {
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+    __device__ __forceinline__ void back() {
+        if (--i < 0) {
+            i = N - 1;
+            ph ^= 1;
+        }
+    }
+};
+
+// TMA role, one thread: the blocks kb0 .. kb1 of the rows at ra (RA of them) and rw (RW).
+template <int ST, int RA, int RW>
+__device__ __forceinline__ bool load_blocks(const Waiter &wait, Ring<ST> &r, int &issued, uint32_t base, uint32_t full,
+                                            uint32_t empty, const CUtensorMap *ta, const CUtensorMap *tw, int ra, int rw,
+                                            int kb0, int kb1) {
+    for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait(empty + 8 * r.i, r.ph ^ 1))
+            return false;
+        mbar_arrive_expect_tx(full + 8 * r.i, (RA + RW) * kBK);
+        const uint32_t dst = base + r.i * ((RA + RW) * kBK);
+        tma_load_2d(dst, ta, kb * kBK, ra, full + 8 * r.i);
+        tma_load_2d(dst + RA * kBK, tw, kb * kBK, rw, full + 8 * r.i);
+        issued = issued < ST ? issued + 1 : ST;
+        r.next();
+    }
+    return true;
+}
+
+// After a failed wait: the copies in flight land before the block may end.
+template <int ST> __device__ __forceinline__ void drain_loads(Ring<ST> r, int issued, uint32_t full) {
+    for (int i = 0; i < issued; ++i) {
+        r.back();
+        mbar_wait_bounded(full + 8 * r.i, r.ph, kDefaultWaitLimit);
+    }
+}
+
+// Scale role, two warps: scales of RS consecutive rows of `sc` (row length KB, the last valid row for
+// rows behind `rows`), four blocks at a time, as [slot][4][RS] floats, each times `w` of that block
+// where w is given.
+template <int RS>
+__device__ __forceinline__ bool load_scales(const Waiter &wait, Ring<kScaleSlots> &r, float *ring, uint32_t sfull,
+                                            uint32_t sempty, const float *sc, int64_t first, int64_t rows, int KB,
+                                            const float *w, int kb0, int kb1, int who, int lane) {
+    for (int kb = kb0; kb < kb1; kb += 4) {
+        const bool ok = wait(sempty + 8 * r.i, r.ph ^ 1);
+        if (__any_sync(0xffffffffu, !ok))
+            return false;
+        float *dst = ring + r.i * 4 * RS;
+        for (int row = 32 * who + lane; row < RS; row += 64) {
+            const int64_t at = first + row < rows ? first + row : rows - 1;
+            const float *src = sc + at * KB + kb;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (kb + 4 <= kb1 && ((uintptr_t)src & 15) == 0) {
+                *reinterpret_cast<float4 *>(v) = __ldg(reinterpret_cast<const float4 *>(src));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (kb + j < kb1)
+                        v[j] = __ldg(src + j);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                dst[j * RS + row] = w != nullptr && kb + j < kb1 ? v[j] * __ldg(w + kb + j) : v[j];
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(sfull + 8 * r.i);
+        r.next();
+    }
+    return true;
+}
+
+// MMA role, one warp: D of buffer b (BN columns) = the block's RA x 128 by RW x 128 product.
+template <int ST, int NB, int RA, int RW, int BN, bool A_IS_W>
+__device__ __forceinline__ bool issue_blocks(const Waiter &wait, Ring<ST> &r, Ring<NB> &d, uint32_t base, uint32_t full,
+                                             uint32_t empty, uint32_t tfull, uint32_t tempty, uint32_t tmem, int blocks,
+                                             uint32_t issue) {
+    for (int kb = 0; kb < blocks; ++kb) {
+        const bool ok = wait(tempty + 8 * d.i, d.ph ^ 1) && wait(full + 8 * r.i, r.ph);
+        if (__any_sync(0xffffffffu, !ok))
+            return false;
+        tc_fence_after();
+        const uint32_t a = base + r.i * ((RA + RW) * kBK), w = a + RA * kBK;
+#pragma unroll
+        for (int k = 0; k < kBK / 32; ++k)
+            mma_f8_ss_if(tmem + d.i * BN, sdesc_sw128((A_IS_W ? w : a) + 32 * k, 16, 1024),
+                         sdesc_sw128((A_IS_W ? a : w) + 32 * k, 16, 1024), idesc_e4m3(128, BN), k > 0, issue);
+        mma_commit_if(empty + 8 * r.i, issue);
+        mma_commit_if(tfull + 8 * d.i, issue);
+        r.next();
+        d.next();
+    }
+    return true;
+}
+
+// After a failed wait: the MMAs in flight end before their memory is given back.
+template <int NB> __device__ __forceinline__ void drain_mma(const Ring<NB> &d, uint32_t tfull, uint32_t issue) {
+    mma_commit_if(tfull + 8 * d.i, issue);
+    mbar_wait_bounded(tfull + 8 * d.i, d.ph, kDefaultWaitLimit);
+}
+
+// 64 columns of one row from registers to out.
 template <typename O>
-__device__ __forceinline__ void store_row(const MatmulArgs &p, int64_t m, int64_t n0, const unsigned long long (&acc)[64],
+__device__ __forceinline__ void store_row(const MatmulArgs &p, int64_t m, int64_t n0, const unsigned long long (&acc)[32],
                                           bool vec) {
     O *dst = reinterpret_cast<O *>(p.out) + m * p.out_stride + n0;
     constexpr int V = 16 / sizeof(O);
-    if (vec && n0 + 128 <= p.N) {
+    if (vec && n0 + 64 <= p.N) {
 #pragma unroll
-        for (int i = 0; i < 128; i += V) {
+        for (int i = 0; i < 64; i += V) {
             Vec16<O> v;
 #pragma unroll
             for (int k = 0; k < V; k += 2) {
@@ -107,7 +228,7 @@ __device__ __forceinline__ void store_row(const MatmulArgs &p, int64_t m, int64_
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < 32; ++i) {
             const float2 f = unpack2(acc[i]);
             if (n0 + 2 * i < p.N)
                 dst[2 * i] = from_f<O>(f.x);
@@ -129,30 +250,29 @@ __device__ __forceinline__ void tile_of(int64_t t, int tiles_m, int tiles_n, int
     tn = (int)(r / rows);
 }
 
-// Persistent over tiles (ks = 1), or one tile per cluster of ks blocks that
-// share its blocks of k and join their sums through shared memory.
-// Warp 0 loads, warp 1 issues the MMAs; the other warpgroups each take 128
-// columns: a thread adds its row's finished block to 128 register sums while
-// the tensor core works on the next one in the other half of TMEM.
-template <int BN, typename O>
-__global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
+constexpr int kWideN = 256, kWideStages = 4, kWideThreads = 640;
+constexpr size_t kWideSmem = 1024 + (size_t)kWideStages * (128 + kWideN) * kBK;
+
+// Four warpgroups take 64 columns each: a thread adds its row's finished block
+// to 64 register sums while the tensor core works on the next one in the other
+// half of TMEM.  Reading TMEM is latency that only other warps hide: two
+// warpgroups of 128 columns took 146 us at 4096 x 12352 x 2048, four take 128.
+template <typename O>
+__global__ void __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tw, const MatmulArgs p,
-                int tiles_m, int tiles_n, int ks, uint32_t *status) {
-    using W = Wide<BN>;
-    constexpr int ST = W::kStages;
+                int tiles_m, int tiles_n, uint32_t *status) {
+    constexpr int ST = kWideStages, BN = kWideN;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * ST + 4];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 4 + 2 * kScaleSlots];
+    __shared__ float scales[kScaleSlots * 4 * 128];
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * ST, tfull = empty + 8 * ST, tempty = tfull + 16;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * ST, tfull = empty + 8 * ST, tempty = tfull + 16,
+                   sfull = tempty + 16, sempty = sfull + 8 * kScaleSlots;
     const int64_t tiles = (int64_t)tiles_m * tiles_n;
     const int KB = (int)((p.K + kBK - 1) / kBK);
-    const int part = ks > 1 ? (int)cluster_rank() : 0;
-    const int kb0 = (int)((int64_t)KB * part / ks), kb1 = (int)((int64_t)KB * (part + 1) / ks);
-    const int64_t t0 = blockIdx.x / ks, dt = gridDim.x / ks;
-    volatile uint32_t *abort_v = &abort_flag;
-
+    const Waiter wait{&abort_flag, status};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -160,7 +280,11 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1);
-            mbar_init(tempty + 8 * i, 4 * W::kGroups);
+            mbar_init(tempty + 8 * i, 16);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(sfull + 8 * i, 2);
+            mbar_init(sempty + 8 * i, 16);
         }
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -173,329 +297,399 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    // A wait that runs out (about a second) makes every role stop at its next
-    // wait; what is in flight is waited for below, and the status word says so.
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (mbar_try_wait_spin(bar, parity))
-            return true;
-        if (!*abort_v && mbar_wait_bounded(bar, parity, kDefaultWaitLimit))
-            return true;
-        *abort_v = 1;
-        atomicOr(status, kStatusTimeout);
-        return false;
-    };
-
+    bool ok = true;
+    int tm, tn;
     if (warp < 4) {
-        if (BN == 256)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // 128 x 32 + 512 x 112 registers are what the block was launched with (640 x 96)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
         if (warp == 0 && lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
+            Ring<ST> r;
             int issued = 0;
-            for (int64_t t = t0; ok && t < tiles; t += dt) {
-                int tm, tn;
+            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 tile_of(t, tiles_m, tiles_n, tm, tn);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = wait(empty + 8 * s, ph ^ 1)))
-                        break;
-                    mbar_arrive_expect_tx(full + 8 * s, W::kStageBytes);
-                    const uint32_t dst = base + s * W::kStageBytes;
-                    tma_load_2d(dst, &ta, kb * kBK, tm * 128, full + 8 * s);
-                    tma_load_2d(dst + kABytes, &tw, kb * kBK, tn * BN, full + 8 * s);
-                    issued = issued < ST ? issued + 1 : ST;
-                    if (++s == ST) {
-                        s = 0;
-                        ph ^= 1;
-                    }
-                }
+                ok = load_blocks<ST, 128, BN>(wait, r, issued, base, full, empty, &ta, &tw, tm * 128, tn * BN, 0, KB);
             }
-            if (!ok) { // the copies in flight land before the block may end
-                for (int i = 0; i < issued; ++i) {
-                    if (--s < 0) {
-                        s = ST - 1;
-                        ph ^= 1;
-                    }
-                    mbar_wait_bounded(full + 8 * s, ph, kDefaultWaitLimit);
-                }
-            }
+            if (!ok)
+                drain_loads(r, issued, full);
         } else if (warp == 1) {
             const uint32_t issue = elect_one();
-            int s = 0, b = 0;
-            uint32_t ph = 0, bph = 0;
-            bool ok = true;
-            for (int64_t t = t0; ok && t < tiles; t += dt) {
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = wait(tempty + 8 * b, bph ^ 1) && wait(full + 8 * s, ph)))
-                        break;
-                    tc_fence_after();
-                    const uint32_t at = base + s * W::kStageBytes;
-#pragma unroll
-                    for (int k = 0; k < kBK / 32; ++k)
-                        mma_f8_ss_if(tmem + b * BN, sdesc_sw128(at + 32 * k, 16, 1024),
-                                     sdesc_sw128(at + kABytes + 32 * k, 16, 1024), idesc_e4m3(128, BN), k > 0, issue);
-                    mma_commit_if(empty + 8 * s, issue);
-                    mma_commit_if(tfull + 8 * b, issue);
-                    if (++s == ST) {
-                        s = 0;
-                        ph ^= 1;
-                    }
-                    if (++b == 2) {
-                        b = 0;
-                        bph ^= 1;
-                    }
-                }
-            }
-            if (!ok) { // the MMAs in flight end before their memory is given back
-                mma_commit_if(tfull + 8 * b, issue);
-                mbar_wait_bounded(tfull + 8 * b, bph, kDefaultWaitLimit);
+            Ring<ST> r;
+            Ring<2> d;
+            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x)
+                ok = issue_blocks<ST, 2, 128, BN, BN, false>(wait, r, d, base, full, empty, tfull, tempty, tmem, KB, issue);
+            if (!ok)
+                drain_mma(d, tfull, issue);
+        } else if (warp >= 2) {
+            Ring<kScaleSlots> r;
+            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                tile_of(t, tiles_m, tiles_n, tm, tn);
+                ok = load_scales<128>(wait, r, scales, sfull, sempty, p.a_scale, (int64_t)tm * 128, p.M, KB, nullptr, 0,
+                                      KB, warp - 2, lane);
             }
         }
     } else {
-        if (BN == 256)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         const int wg = (warp - 4) >> 2, q = warp & 3; // TMEM lanes 32 q .. of this warp
         const bool vec = ((uintptr_t)p.out & 15) == 0 && (p.out_stride * sizeof(O)) % 16 == 0;
-        int b = 0;
-        uint32_t bph = 0;
-        bool ok = true;
-        for (int64_t t = t0; ok && t < tiles; t += dt) {
-            int tm, tn;
+        Ring<2> d;
+        Ring<kScaleSlots> r;
+        for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
             tile_of(t, tiles_m, tiles_n, tm, tn);
-            const int64_t m = (int64_t)tm * 128 + 32 * q + lane, n0 = (int64_t)tn * BN + 128 * wg;
-            // rows and columns behind the end have zero operands; their scales are any valid ones
-            const float *sa = p.a_scale + (m < p.M ? m : p.M - 1) * KB;
+            const int64_t m = (int64_t)tm * 128 + 32 * q + lane, n0 = (int64_t)tn * BN + 64 * wg;
+            // columns behind the end have zero operands; their scale is any valid one
             const float *sw = p.w_scale + (n0 < p.N ? n0 / 128 : 0) * KB;
-            unsigned long long acc[64];
+            unsigned long long acc[32];
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
+            for (int i = 0; i < 32; ++i)
                 acc[i] = 0ull;
-            float next = kb0 < kb1 ? __ldg(sa + kb0) * __ldg(sw + kb0) : 0.f;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                const unsigned long long sc = pack2(next, next);
-                if (kb + 1 < kb1)
-                    next = __ldg(sa + kb + 1) * __ldg(sw + kb + 1);
-                ok = wait(tfull + 8 * b, bph);
+            float w = __ldg(sw);
+            for (int kb = 0; kb < KB; ++kb) {
+                if ((kb & 3) == 0) {
+                    ok = wait(sfull + 8 * r.i, r.ph);
+                    if (__any_sync(0xffffffffu, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                const float f = w * scales[(r.i * 4 + (kb & 3)) * 128 + 32 * q + lane];
+                const unsigned long long sc = pack2(f, f);
+                if (kb + 1 < KB)
+                    w = __ldg(sw + kb + 1);
+                if ((kb & 3) == 3 || kb + 1 == KB) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(sempty + 8 * r.i);
+                    r.next();
+                }
+                ok = wait(tfull + 8 * d.i, d.ph);
                 if (__any_sync(0xffffffffu, !ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = tmem + b * BN + 128 * wg + ((uint32_t)(32 * q) << 16);
+                const uint32_t at = tmem + d.i * BN + 64 * wg + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     float v[32];
                     tmem_ld32(at + 32 * c, v);
                     tmem_wait_ld();
-                    if (c == 3) { // all of this half of TMEM is read
+                    if (c == 1) { // all of this half of TMEM is read
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(tempty + 8 * b);
+                            mbar_arrive(tempty + 8 * d.i);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         fma2(acc[16 * c + i], sc, pack2(v[2 * i], v[2 * i + 1]));
                 }
-                if (++b == 2) {
-                    b = 0;
-                    bph ^= 1;
-                }
+                d.next();
             }
-            if (ks == 1) {
-                if (ok && m < p.M)
-                    store_row<O>(p, m, n0, acc, vec);
-            } else {
-                // own sums to the (now idle) stages; the odd row length keeps the banks apart
-                float *dst = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)));
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const float2 f = unpack2(acc[i]);
-                    dst[(32 * q + lane) * (BN + 1) + 128 * wg + 2 * i] = f.x;
-                    dst[(32 * q + lane) * (BN + 1) + 128 * wg + 2 * i + 1] = f.y;
-                }
-            }
+            if (ok && m < p.M)
+                store_row<O>(p, m, n0, acc, vec);
         }
     }
     __syncwarp();
     __syncthreads();
-    if (ks > 1) {
-        // this block sums its share of the columns over the cluster, in the order of k
-        cluster_sync();
-        const int64_t t = t0;
-        int tm, tn;
-        tile_of(t, tiles_m, tiles_n, tm, tn);
-        const int cols = BN / ks, c0 = cols * part;
-        for (int i = tid; i < cols * 128; i += W::kThreads) {
-            const int c = i % cols, r = i / cols;
-            const int64_t m = (int64_t)tm * 128 + r, n = (int64_t)tn * BN + c0 + c;
-            if (m < p.M && n < p.N) {
-                float v = 0.f;
-                for (int k = 0; k < ks; ++k)
-                    v += ld_dsmem(base + 4u * (r * (BN + 1) + c0 + c), k);
-                reinterpret_cast<O *>(p.out)[m * p.out_stride + n] = from_f<O>(v);
-            }
-        }
-        cluster_sync(); // the others may still be reading this block's sums
-    }
     if (warp == 1) {
         tmem_relinquish();
         tmem_dealloc(tmem, 2 * BN);
     }
 }
 
-template <int BN, typename O> cudaError_t go_wide(const MatmulArgs &p, int tiles_m, int tiles_n, int ks, cudaStream_t s) {
-    using W = Wide<BN>;
+template <typename O> cudaError_t go_wide(const MatmulArgs &p, cudaStream_t s) {
+    const int tiles_m = (int)((p.M + 127) / 128), tiles_n = (int)((p.N + kWideN - 1) / kWideN);
     CUtensorMap ta, tw;
     if (!encode_2d(&ta, p.a, p.K, p.M, p.K, kBK, 128, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-        !encode_2d(&tw, p.w, p.K, p.N, p.K, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        !encode_2d(&tw, p.w, p.K, p.N, p.K, kBK, kWideN, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(wide_kernel<BN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(wide_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWideSmem);
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = (int64_t)tiles_m * tiles_n;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(ks > 1 ? tiles * ks : (tiles < kSMs ? tiles : kSMs)));
-    cfg.blockDim = dim3(W::kThreads);
-    cfg.dynamicSmemBytes = W::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, wide_kernel<BN, O>, ta, tw, p, tiles_m, tiles_n, ks,
-                              reinterpret_cast<uint32_t *>(p.ws));
-}
-
-// ------------------------------------------------------------------ narrow
-
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-constexpr int kNarrowWarps = 8;
-
-// Up to 8 NT rows of a.  A warp takes 16 rows of w and a share of the blocks of
-// k: the 16 rows are the M of m16n8k32, the rows of a its N.  Both operands
-// take 16 consecutive bytes of k per thread where the instruction's layout
-// names 4 scattered groups of 4: the same permutation of k on both sides, so
-// the sum is the same and every load is 16 bytes wide.
-// wk warps of a block share 16 rows of w and join in shared memory.
-template <int NT, typename O>
-__global__ void __launch_bounds__(kNarrowWarps * 32) narrow_kernel(const MatmulArgs p, int wk) {
-    __shared__ float sums[kNarrowWarps][NT * 4][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rows = kNarrowWarps / wk; // 16-row groups of the block
-    const int64_t n0 = ((int64_t)blockIdx.x * rows + warp / wk) * 16;
-    const int KB = (int)((p.K + kBK - 1) / kBK), part = warp % wk;
-    const int kb0 = (int)((int64_t)KB * part / wk), kb1 = (int)((int64_t)KB * (part + 1) / wk);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float acc[NT][4] = {};
-    if (n0 < p.N) {
-        const uint8_t *w0 = reinterpret_cast<const uint8_t *>(p.w) + (n0 + g) * p.K + 16 * t;
-        const uint8_t *w1 = w0 + 8 * p.K;
-        const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
-        const uint8_t *a = reinterpret_cast<const uint8_t *>(p.a) + g * p.K + 16 * t;
-        const float *sw = p.w_scale + n0 / 128 * KB;
-#pragma unroll 2
-        for (int kb = kb0; kb < kb1; ++kb) {
-            uint4 wr[2][2], ar[2][NT];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t k = (int64_t)kb * kBK + 64 * h;
-                const bool in = k + 16 * t < p.K;
-                wr[h][0] = in && in0 ? __ldcs(reinterpret_cast<const uint4 *>(w0 + k)) : zero;
-                wr[h][1] = in && in1 ? __ldcs(reinterpret_cast<const uint4 *>(w1 + k)) : zero;
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    ar[h][i] = in && 8 * i + g < p.M ? __ldg(reinterpret_cast<const uint4 *>(a + 8 * i * p.K + k)) : zero;
-            }
-            const float s = __ldg(sw + kb);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mma_e4m3(c, wr[h][0].x, wr[h][1].x, wr[h][0].y, wr[h][1].y, ar[h][i].x, ar[h][i].y);
-                    mma_e4m3(c, wr[h][0].z, wr[h][1].z, wr[h][0].w, wr[h][1].w, ar[h][i].z, ar[h][i].w);
-                }
-                const int m = 8 * i + 2 * t;
-                const float s0 = m < p.M ? s * __ldg(p.a_scale + (int64_t)m * KB + kb) : 0.f;
-                const float s1 = m + 1 < p.M ? s * __ldg(p.a_scale + (int64_t)(m + 1) * KB + kb) : 0.f;
-                acc[i][0] = fmaf(s0, c[0], acc[i][0]);
-                acc[i][1] = fmaf(s1, c[1], acc[i][1]);
-                acc[i][2] = fmaf(s0, c[2], acc[i][2]);
-                acc[i][3] = fmaf(s1, c[3], acc[i][3]);
-            }
-        }
-    }
-    if (wk > 1) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sums[warp][4 * i + e][lane] = acc[i][e];
-        __syncthreads();
-        if (part != 0)
-            return;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                for (int k = 1; k < wk; ++k)
-                    acc[i][e] += sums[warp + k][4 * i + e][lane];
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t m = 8 * i + 2 * t + (e & 1), n = n0 + g + 8 * (e >> 1);
-            if (m < p.M && n < p.N)
-                reinterpret_cast<O *>(p.out)[m * p.out_stride + n] = from_f<O>(acc[i][e]);
-        }
-}
-
-template <int NT, typename O> cudaError_t go_narrow(const MatmulArgs &p, cudaStream_t s) {
-    const int64_t groups = (p.N + 15) / 16;
-    const int KB = (int)((p.K + kBK - 1) / kBK);
-    // enough warps to keep some 40 KB of w in flight on every SM, at least one block of k each
-    int wk = 1;
-    while (wk < kNarrowWarps && groups * wk < 16 * kSMs && 2 * wk <= KB)
-        wk *= 2;
-    const int rows = kNarrowWarps / wk;
-    narrow_kernel<NT, O><<<(unsigned)((groups + rows - 1) / rows), kNarrowWarps * 32, 0, s>>>(p, wk);
+    wide_kernel<O><<<(unsigned)(tiles < kSMs ? tiles : kSMs), kWideThreads, kWideSmem, s>>>(
+        ta, tw, p, tiles_m, tiles_n, reinterpret_cast<uint32_t *>(p.ws));
     return cudaGetLastError();
 }
 
-template <typename O> cudaError_t launch_t(const MatmulArgs &p, cudaStream_t s) {
-    if (p.M <= 8)
-        return go_narrow<1, O>(p, s);
-    if (p.M <= 16)
-        return go_narrow<2, O>(p, s);
-    if (p.M <= 32)
-        return go_narrow<4, O>(p, s);
-    const int tiles_m = (int)((p.M + 127) / 128);
+// ------------------------------------------------------------------- thin
+
+template <int BN> struct Thin {
+    static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 8 : BN == 32 ? 9 : 11;
+    static constexpr int kBuffers = BN == 16 ? 8 : 4;     // accumulators in TMEM
+    static constexpr int kTmem = BN * kBuffers;
+    static constexpr int kGroups = BN == 128 ? 2 : 1;     // warpgroups that add, each BN / kGroups columns
+    static constexpr int kThreads = 128 + 128 * kGroups;
+    static constexpr size_t kStageBytes = (size_t)kStages * (128 + BN) * kBK;
+    static constexpr size_t kJoinBytes = 136 * (BN + 4) * 4; // ks join_rows(ks) <= 133 rows, 16 bytes apart in banks
+    static constexpr size_t kSmem = 1024 + (kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes);
+};
+
+// Rows of a tile that a block of the cluster adds up, at most.
+__device__ __forceinline__ int join_rows(int ks) { return (128 + ks - 1) / ks; }
+
+// One tile per cluster of ks blocks, which split its blocks of k and join their
+// sums through shared memory, in the order of k.  A thread has one row of w
+// and BN / kGroups rows of a.
+template <int BN, typename O>
+__global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
+    thin_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tw, const MatmulArgs p,
+                int tiles_n, int ks, uint32_t *status) {
+    using T = Thin<BN>;
+    constexpr int ST = T::kStages, NB = T::kBuffers, COLS = BN / T::kGroups, LD = COLS < 32 ? COLS : 32;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 2 * NB + 2 * kScaleSlots];
+    __shared__ __align__(16) float scales[kScaleSlots * 4 * BN];
+    __shared__ uint32_t tmem_base, abort_flag;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    float *join = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * ST, tfull = empty + 8 * ST, tempty = tfull + 8 * NB,
+                   sfull = tempty + 8 * NB, sempty = sfull + 8 * kScaleSlots;
     const int KB = (int)((p.K + kBK - 1) / kBK);
-    const int64_t wide = (int64_t)tiles_m * ((p.N + 255) / 256);
-    if (wide >= kSMs)
-        return go_wide<256, O>(p, tiles_m, (int)((p.N + 255) / 256), 1, s);
-    const int tiles_n = (int)((p.N + 127) / 128);
-    const int64_t tiles = (int64_t)tiles_m * tiles_n;
-    int ks = 1;
-    while (ks < 8 && tiles * ks * 2 <= kSMs && 2 * ks <= KB)
-        ks *= 2;
-    return go_wide<128, O>(p, tiles_m, tiles_n, ks, s);
+    const int part = ks > 1 ? (int)cluster_rank() : 0;
+    const int kb0 = KB * part / ks, kb1 = KB * (part + 1) / ks;
+    const int tile = blockIdx.x / ks, tm = tile / tiles_n, tn = tile % tiles_n;
+    const int64_t m0 = (int64_t)tm * BN, n0 = (int64_t)tn * 128;
+    const Waiter wait{&abort_flag, status};
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(tfull + 8 * i, 1);
+            mbar_init(tempty + 8 * i, 4 * T::kGroups);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(sfull + 8 * i, 2);
+            mbar_init(sempty + 8 * i, 4 * T::kGroups);
+        }
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (blockIdx.x == 0)
+            *status = 0;
+    }
+    if (warp == 1)
+        tmem_alloc(smem_u32(&tmem_base), T::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            Ring<ST> r;
+            int issued = 0;
+            if (!load_blocks<ST, BN, 128>(wait, r, issued, base, full, empty, &ta, &tw, (int)m0, (int)n0, kb0, kb1))
+                drain_loads(r, issued, full);
+        }
+    } else if (warp == 1) {
+        const uint32_t issue = elect_one();
+        Ring<ST> r;
+        Ring<NB> d;
+        if (!issue_blocks<ST, NB, BN, 128, BN, true>(wait, r, d, base, full, empty, tfull, tempty, tmem, kb1 - kb0, issue))
+            drain_mma(d, tfull, issue);
+    } else if (warp < 4) {
+        Ring<kScaleSlots> r;
+        load_scales<BN>(wait, r, scales, sfull, sempty, p.a_scale, m0, p.M, KB, p.w_scale + (int64_t)tn * KB, kb0, kb1,
+                        warp - 2, lane);
+    } else {
+        const int wg = (warp - 4) >> 2, q = warp & 3;
+        Ring<NB> d;
+        Ring<kScaleSlots> r;
+        unsigned long long acc[COLS / 2];
+#pragma unroll
+        for (int i = 0; i < COLS / 2; ++i)
+            acc[i] = 0ull;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const int j = (kb - kb0) & 3;
+            ok = (j != 0 || wait(sfull + 8 * r.i, r.ph)) && wait(tfull + 8 * d.i, d.ph);
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t at = tmem + d.i * BN + COLS * wg + ((uint32_t)(32 * q) << 16);
+            const ulonglong2 *sc = reinterpret_cast<const ulonglong2 *>(scales + (r.i * 4 + j) * BN + COLS * wg);
+#pragma unroll
+            for (int c = 0; c < COLS; c += LD) {
+                float v[LD];
+                if constexpr (LD == 16)
+                    tmem_ld16(at + c, v);
+                else
+                    tmem_ld32(at + c, v);
+                tmem_wait_ld();
+                if (c + LD == COLS) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(tempty + 8 * d.i);
+                }
+#pragma unroll
+                for (int i = 0; i < LD / 4; ++i) {
+                    const ulonglong2 s2 = sc[c / 4 + i];
+                    fma2(acc[c / 2 + 2 * i], s2.x, pack2(v[4 * i], v[4 * i + 1]));
+                    fma2(acc[c / 2 + 2 * i + 1], s2.y, pack2(v[4 * i + 2], v[4 * i + 3]));
+                }
+            }
+            d.next();
+            if (j == 3 || kb + 1 == kb1) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(sempty + 8 * r.i);
+                r.next();
+            }
+        }
+        const int row = 32 * q + lane;
+        if (ks == 1) {
+            const int64_t n = n0 + row;
+            if (ok && n < p.N) {
+                O *dst = reinterpret_cast<O *>(p.out) + (m0 + COLS * wg) * p.out_stride + n;
+#pragma unroll
+                for (int i = 0; i < COLS / 2; ++i) {
+                    const float2 f = unpack2(acc[i]);
+                    if (m0 + COLS * wg + 2 * i < p.M)
+                        dst[2 * i * p.out_stride] = from_f<O>(f.x);
+                    if (m0 + COLS * wg + 2 * i + 1 < p.M)
+                        dst[(2 * i + 1) * p.out_stride] = from_f<O>(f.y);
+                }
+            }
+        } else {
+            // each block of the cluster adds up its share of the rows: send it the sums, once the stages,
+            // which hold them, are idle in all blocks
+            cluster_sync();
+            const int to = row * ks / 128, r0 = (128 * to + ks - 1) / ks;
+            const uint32_t dst = mapa(smem_u32(join), to) + 4u * ((part * join_rows(ks) + row - r0) * (BN + 4) + COLS * wg);
+#pragma unroll
+            for (int i = 0; i < COLS / 4; ++i)
+                if (m0 + COLS * wg + 4 * i < p.M)
+                    st_dsmem(dst + 16 * i, acc[2 * i], acc[2 * i + 1]);
+        }
+    }
+    if (warp < 4 && ks > 1) {
+        __syncwarp();
+        cluster_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (ks > 1) {
+        cluster_sync();
+        const int quads = (int)((p.M - m0 < BN ? p.M - m0 : BN) + 3) / 4; // of rows of a that exist
+        const int r0 = (128 * part + ks - 1) / ks, nr = (128 * (part + 1) + ks - 1) / ks - r0;
+        for (int i = tid; i < quads * nr; i += T::kThreads) {
+            const int c = i / nr * 4, r = i % nr;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < ks; ++k) {
+                const float4 u = *reinterpret_cast<const float4 *>(join + (k * join_rows(ks) + r) * (BN + 4) + c);
+                v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+            }
+            const int64_t m = m0 + c, n = n0 + r0 + r;
+            O *dst = reinterpret_cast<O *>(p.out) + m * p.out_stride + n;
+            if (n < p.N) {
+                dst[0] = from_f<O>(v.x);
+                if (m + 1 < p.M)
+                    dst[p.out_stride] = from_f<O>(v.y);
+                if (m + 2 < p.M)
+                    dst[2 * p.out_stride] = from_f<O>(v.z);
+                if (m + 3 < p.M)
+                    dst[3 * p.out_stride] = from_f<O>(v.w);
+            }
+        }
+    }
+    if (warp == 1) {
+        tmem_relinquish();
+        tmem_dealloc(tmem, T::kTmem);
+    }
+}
+
+template <int BN, typename O> cudaLaunchConfig_t thin_config(unsigned blocks, int ks, cudaLaunchAttribute *at, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(Thin<BN>::kThreads);
+    cfg.dynamicSmemBytes = Thin<BN>::kSmem;
+    cfg.stream = s;
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = ks;
+    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of 1 .. 8 blocks that run at once, as the runtime counts them (the
+// SMs of a cluster are of one GPC, so 148 SMs hold fewer clusters of 8 than
+// 18).  Asked once per process; it decides a launch shape only.
+template <int BN, typename O> struct Capacity {
+    int clusters[9] = {};
+    cudaError_t error;
+    Capacity() {
+        error = cudaFuncSetAttribute(thin_kernel<BN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Thin<BN>::kSmem);
+        for (int ks = 1; ks <= 8 && error == cudaSuccess; ++ks) {
+            cudaLaunchAttribute at{};
+            const cudaLaunchConfig_t cfg = thin_config<BN, O>(400 * ks, ks, &at, nullptr);
+            error = cudaOccupancyMaxActiveClusters(&clusters[ks], thin_kernel<BN, O>, &cfg);
+        }
+    }
+};
+
+// Blocks of a cluster for this many tiles and blocks of k: the most that still
+// all run at once, with two blocks of k each at least.
+template <int BN, typename O> cudaError_t thin_split(int64_t tiles, int KB, int *ks) {
+    static const Capacity<BN, O> cap;
+    *ks = 1;
+    for (int k = 2; k <= 8 && 2 * k <= KB; ++k)
+        if (tiles <= cap.clusters[k])
+            *ks = k;
+    return cap.error;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int BN, typename O> cudaError_t go_thin(const MatmulArgs &p, cudaStream_t s) {
+    using T = Thin<BN>;
+    const int64_t tiles_n = ceil_div(p.N, 128), tiles = ceil_div(p.M, BN) * tiles_n;
+    int ks;
+    cudaError_t e = thin_split<BN, O>(tiles, (int)ceil_div(p.K, kBK), &ks);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(thin_kernel<BN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    CUtensorMap ta, tw;
+    if (!encode_2d(&ta, p.a, p.K, p.M, p.K, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+        !encode_2d(&tw, p.w, p.K, p.N, p.K, kBK, 128, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        return cudaErrorInvalidValue;
+    cudaLaunchAttribute at{};
+    const cudaLaunchConfig_t cfg = thin_config<BN, O>((unsigned)(tiles * ks), ks, &at, s);
+    return cudaLaunchKernelEx(&cfg, thin_kernel<BN, O>, ta, tw, p, (int)tiles_n, ks, reinterpret_cast<uint32_t *>(p.ws));
+}
+
+template <typename O> cudaError_t launch_t(const MatmulArgs &p, cudaStream_t s) {
+    if (p.M <= 16)
+        return go_thin<16, O>(p, s);
+    if (p.M <= 32)
+        return go_thin<32, O>(p, s);
+    if (p.M <= 64)
+        return go_thin<64, O>(p, s);
+    // Both kernels take 0.5 to 0.6 us for a block of k, the wide one for twice
+    // the columns; the one whose busiest SM has fewer blocks runs (the thin one
+    // if equal: 14.0 us against 15.5 at 128 x 12352 x 2048).  At 512 x 8192
+    // x 8192 that is the wide one (128 tiles in one round, 64 blocks; thin: 256
+    // tiles in two rounds; 37 us against 66), at 301 x 1003 x 4112 the thin one (24 tiles in
+    // 5 parts, 7 blocks, 12 us; wide: 12 tiles of 33 blocks).
+    const int64_t KB = ceil_div(p.K, kBK), tm = ceil_div(p.M, 128), tt = tm * ceil_div(p.N, 128);
+    int ks;
+    const cudaError_t e = thin_split<128, O>(tt, (int)KB, &ks);
+    if (e != cudaSuccess)
+        return e;
+    if (ceil_div(tm * ceil_div(p.N, kWideN), kSMs) * KB < ceil_div(tt * ks, kSMs) * ceil_div(KB, ks))
+        return go_wide<O>(p, s);
+    return go_thin<128, O>(p, s);
 }
 
 } // namespace
 
-// The first word of the workspace is the status word of the wide kernel.
+// The first word of the workspace is the kernels' status word.
 size_t matmul_workspace_bytes(int64_t, int64_t, int64_t) { return kWorkspaceHeader; }
 
 cudaError_t launch_matmul(const MatmulArgs &p, cudaStream_t s) {

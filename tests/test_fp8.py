@@ -145,7 +145,7 @@ def check_product(out, a, sa, w, sw):
 
 SHAPES = [(1, 1, 16), (1, 128, 128), (2, 129, 144), (3, 257, 112), (5, 7, 4112), (16, 384, 1024), (17, 130, 272),
           (33, 1000, 512), (64, 127, 640), (65, 256, 2048), (127, 12, 128), (128, 128, 256), (129, 255, 1040),
-          (1537, 3331, 400), (2100, 2400, 128), (200, 640, 768), (257, 513, 384), (300, 1032, 144), (1, 4096, 2048), (8, 520, 8192)]
+          (1537, 3331, 400), (31, 300, 2064), (50, 1030, 1552), (2100, 2400, 128), (200, 640, 768), (257, 513, 384), (300, 1032, 144), (1, 4096, 2048), (8, 520, 8192)]
 
 
 @pytest.mark.gpu
