@@ -153,8 +153,11 @@ struct SsmArgs {
     void *conv_cache = nullptr;  // decode: resident windows
     const float *conv_w, *conv_b, *A_log, *dt_bias, *D;
     void *ws = nullptr;
+    int segments = 1;            // prefill: segments per sequence
     constexpr int conv_dim() const { return H * P + 2 * G * S; }
 };
+int ssm_segments(const gdn_ssm_config *c, int batch, int64_t N); // the call's own, or the library's choice
+bool ssm_addressable(const gdn_ssm_config *c, int batch, int64_t N);
 size_t ssm_workspace_bytes(const gdn_ssm_config *c, int batch, int64_t N);
 cudaError_t launch_ssm_prefill(const SsmArgs &p, cudaEvent_t begin, cudaEvent_t end, cudaStream_t s);
 cudaError_t launch_ssm_decode(const SsmArgs &p, cudaStream_t s);

@@ -98,7 +98,7 @@ gdn_status gdn_ssm_prefill_workspace_size(const gdn_ssm_config *cfg, int32_t bat
         return st;
     if (bytes == nullptr || batch < 0 || total_tokens < 0 || (batch == 0 && total_tokens > 0))
         return GDN_ERR_INVALID_ARG;
-    if (total_tokens > INT32_MAX) // cu_seqlens is int32
+    if (batch > 65535 || total_tokens > INT32_MAX || !ssm_addressable(cfg, batch, total_tokens)) // cu_seqlens is int32
         return GDN_ERR_UNSUPPORTED;
     *bytes = ssm_workspace_bytes(cfg, batch, total_tokens);
     return GDN_OK;
@@ -117,7 +117,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *para
     if (batch < 0 || total_tokens < 0 || (batch == 0 && total_tokens > 0) ||
         (batch > 0 && cu_seqlens == nullptr))
         return GDN_ERR_INVALID_ARG;
-    if (batch > 65535 || total_tokens > INT32_MAX)
+    if (batch > 65535 || total_tokens > INT32_MAX || !ssm_addressable(cfg, batch, total_tokens))
         return GDN_ERR_UNSUPPORTED;
     if ((st = check_ssm_rows(cfg, xbc, xbc_stride, dt, dt_stride, z, z_stride, y, total_tokens)) != GDN_OK)
         return st;
@@ -138,6 +138,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *para
     p.final_state = final_state;
     p.final_conv = final_conv;
     p.ws = workspace;
+    p.segments = ssm_segments(cfg, batch, total_tokens);
     return cuda_status(launch_ssm_prefill(p, hook.begin, hook.end, (cudaStream_t)stream));
 }
 
