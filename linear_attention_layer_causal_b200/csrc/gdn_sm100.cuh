@@ -54,6 +54,26 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return true;
 }
 
+// mbar_wait_bounded with polls that let the warp sleep (up to `ns` each) until
+// the phase completes: for kernels whose waiting warps share a scheduler with
+// working ones, which polling would rob of issue slots.
+__device__ __forceinline__ bool mbar_wait_sleeping(uint32_t bar, uint32_t parity, long long limit, uint32_t ns = 2000) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.b32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity), "r"(ns)
+                     : "memory");
+        if (ok)
+            return true;
+        if (clock64() - t0 > limit)
+            return false;
+    }
+}
+
 // Arrive on `bar` expecting `bytes` more bytes of asynchronous (TMA) traffic.
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)

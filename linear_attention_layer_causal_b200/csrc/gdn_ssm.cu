@@ -100,6 +100,8 @@ template <typename T> __device__ __forceinline__ const T *conv_row(const SsmArgs
     return reinterpret_cast<const T *>(p.init_conv) + ((int64_t)n * 3 + 3 + (t - start)) * p.conv_dim();
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ------------------------------------------------------------------- prep
 
 constexpr int kPrepThreads = 256;
@@ -127,10 +129,6 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
                                                                 uint32_t *status) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int LDS = S + 8; // row length in shared memory: rows 16 bytes apart in banks
-    __nv_bfloat16 *part[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        part[i] = reinterpret_cast<__nv_bfloat16 *>(smem) + i * kQ * LDS;
     const int64_t id = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (id == 0 && g == 0 && tid == 0)
@@ -170,24 +168,25 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
             b = __ldg(reinterpret_cast<const float4 *>(p.conv_b + c));
         float4 win[RUN + 3];
 #pragma unroll
-        for (int i = 0; i < RUN + 3; ++i) {
-            win[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r0 + i - 3 < ntok) {
-                const T *row = conv_row<T>(p, n, start, t0 + r0 + i - 3);
-                if (row != nullptr)
-                    win[i] = load4(row + c);
-            }
+        for (int i = 0; i < RUN + 3; ++i) { // unconditional loads: all in flight together
+            const int t = min(r0 + i - 3, ntok - 1);
+            const T *row = conv_row<T>(p, n, start, t0 + t);
+            win[i] = load4((row != nullptr ? row : reinterpret_cast<const T *>(p.xbc) + t0 * p.xbc_stride) + c);
         }
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (p.init_conv == nullptr && t0 + r0 + i - 3 < start)
+                win[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        __nv_bfloat16 *mine = reinterpret_cast<__nv_bfloat16 *>(smem) + (2 * which * kQ + r0) * LDS + col; // hi; lo is kQ rows on
         __nv_bfloat16 *out = bc + ((id * p.G + g) * kQ + r0) * (4 * S) + which * 2 * S + col;
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
+            const float4 ra = win[i], rb = win[i + 1], rc = win[i + 2], rd = win[i + 3];
             float v[4];
-            const float *r[4] = {&win[i].x, &win[i + 1].x, &win[i + 2].x, &win[i + 3].x};
-            const float *ws[4] = {&w[0].x, &w[1].x, &w[2].x, &w[3].x};
-            const float *bs = &b.x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = fmaf(ws[k][3], r[3][k], fmaf(ws[k][2], r[2][k], fmaf(ws[k][1], r[1][k], fmaf(ws[k][0], r[0][k], bs[k]))));
+            v[0] = fmaf(w[0].w, rd.x, fmaf(w[0].z, rc.x, fmaf(w[0].y, rb.x, fmaf(w[0].x, ra.x, b.x))));
+            v[1] = fmaf(w[1].w, rd.y, fmaf(w[1].z, rc.y, fmaf(w[1].y, rb.y, fmaf(w[1].x, ra.y, b.y))));
+            v[2] = fmaf(w[2].w, rd.z, fmaf(w[2].z, rc.z, fmaf(w[2].y, rb.z, fmaf(w[2].x, ra.z, b.z))));
+            v[3] = fmaf(w[3].w, rd.w, fmaf(w[3].z, rc.w, fmaf(w[3].y, rb.w, fmaf(w[3].x, ra.w, b.w))));
             silu2(v[0], v[1]);
             silu2(v[2], v[3]);
             if (r0 + i >= ntok)
@@ -197,8 +196,8 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
             split2(v[2], v[3], h.y, l.y);
             *reinterpret_cast<uint2 *>(out + i * (4 * S)) = h;
             *reinterpret_cast<uint2 *>(out + i * (4 * S) + S) = l;
-            *reinterpret_cast<uint2 *>(part[2 * which] + (r0 + i) * LDS + col) = h;
-            *reinterpret_cast<uint2 *>(part[2 * which + 1] + (r0 + i) * LDS + col) = l;
+            *reinterpret_cast<uint2 *>(mine + i * LDS) = h;
+            *reinterpret_cast<uint2 *>(mine + (kQ + i) * LDS) = l;
         }
     }
 
@@ -303,6 +302,17 @@ __device__ __forceinline__ void mma_bf16_ts_if(uint32_t d, uint32_t a, uint64_t 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
 // Untiled bulk copy of `bytes` (a multiple of 16, both ends 16-byte aligned).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -315,8 +325,8 @@ template <int P, int S> struct Scan {
     static constexpr int kStages = 2;           // chunks of B and C in shared memory
     static constexpr int kGateSlots = 4;
     static constexpr int kStageBytes = 4 * S * kQ * 2;
-    static constexpr int kMBytes = kHeads * 2 * kQ * kQ * 2; // M hi, lo of each head
-    static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kMBytes;
+    static constexpr int kMBytes = kHeads * 2 * kQ * kQ * 2; // M hi, lo of each head; two buffers
+    static constexpr size_t kSmem = 1024 + kStages * kStageBytes + 2 * kMBytes;
     // TMEM columns
     static constexpr uint32_t kDH = 0;             // x' B^T, then H hi and lo of the next chunk
     static constexpr uint32_t kYI = 128;           // H C^T
@@ -324,10 +334,11 @@ template <int P, int S> struct Scan {
     static constexpr uint32_t kXP = 320;           // x' hi, lo
     static constexpr uint32_t kX = 384;            // x hi, lo
 };
-constexpr int kScanThreads = 768;
+constexpr int kScanThreads = 896;
 constexpr uint32_t kTmemCols = 512;
 
-enum Bar { kBcFull = 0, kBcEmpty = 2, kGFull = 4, kGEmpty = 8, kXpFull = 12, kXFull, kMFull, kHFull, kUDone, kIDone, kYEmpty, kDrain, kBars };
+// pairs (by the chunk's parity), the gate slots, and single barriers
+enum Bar { kBcFull = 0, kBcEmpty = 2, kMFull = 4, kIDone = 6, kGFull = 8, kGEmpty = 12, kXpFull = 16, kXFull, kHFull, kUDone, kYEmpty, kDrain, kBars };
 
 // What a block works on.
 struct Unit {
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ __align__(16) float gate[K::kGateSlots][NH][kGateRec];
-    __shared__ int bad[2][128]; // first token of a chunk with a non-finite x, per row
+    __shared__ int bad[2][2][128]; // per half of a chunk and row: the first token with a non-finite x
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t mbase = base + K::kStages * K::kStageBytes;
@@ -385,22 +396,22 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     volatile uint32_t *abort_v = &abort_flag;
 
     if (tid == 0) {
-        const int consumers = SUMMARY ? 12 : 20;
+        const int consumers = SUMMARY ? 16 : 26;
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBcFull + i), 1);
             mbar_init(bar(kBcEmpty + i), 1);
+            mbar_init(bar(kMFull + i), 2);
+            mbar_init(bar(kIDone + i), 1);
         }
         for (int i = 0; i < K::kGateSlots; ++i) {
             mbar_init(bar(kGFull + i), 1);
             mbar_init(bar(kGEmpty + i), consumers);
         }
-        mbar_init(bar(kXpFull), 4);
-        mbar_init(bar(kXFull), 4);
-        mbar_init(bar(kMFull), 4);
+        mbar_init(bar(kXpFull), 8);
+        mbar_init(bar(kXFull), 8);
         mbar_init(bar(kHFull), 8);
         mbar_init(bar(kUDone), 1);
-        mbar_init(bar(kIDone), 1);
-        mbar_init(bar(kYEmpty), 4);
+        mbar_init(bar(kYEmpty), 8);
         mbar_init(bar(kDrain), 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -415,9 +426,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     // A wait that runs out (about a second) makes every role stop at its next
     // wait; what is in flight is waited for before the block ends.
     auto wait = [&](int i, uint32_t parity) {
-        bool ok = mbar_try_wait_spin(bar(i), parity);
-        if (!ok && !*abort_v)
-            ok = mbar_wait_bounded(bar(i), parity, kDefaultWaitLimit);
+        const bool ok = !*abort_v && mbar_wait_sleeping(bar(i), parity, kDefaultWaitLimit);
         if (!ok) {
             *abort_v = 1;
             atomicOr(a.status, kStatusTimeout);
@@ -436,7 +445,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const int64_t chan = (int64_t)u.h0 * P + row; // its x channel
 
     if (wg == 0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        // 128 x (64 + 2 x 64 + 2 x 104 + 2 x 48) registers, of 896 x 72 that the block was launched with
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0 && lane == 0) { // ---- loads
             const int gbytes = u.nh * kGateRec * 4;
             int c = 0;
@@ -503,14 +513,14 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 mma_commit_if(bar(kBcEmpty + (c & 1)), issue);
                 mma_commit_if(bar(kUDone), issue);
                 if (!SUMMARY) {
-                    ok = wait_all(kXFull, ph) && wait_all(kMFull, ph);
+                    ok = wait_all(kXFull, ph) && wait_all(kMFull + (c & 1), (c >> 1) & 1);
                     if (!ok)
                         break;
                     tc_fence_after();
                     // I: D[row][t] = sum_{s <= t} x[row][s] M[t][s] for each head's M; all 128 rows take part, a
                     // head's rows read their own.  Tokens before a 16-block of s take nothing from it.
                     for (int h = 0; h < u.nh; ++h) {
-                        const uint32_t mh = mbase + h * 2 * kQ * kQ * 2, ml = mh + kQ * kQ * 2;
+                        const uint32_t mh = mbase + (c & 1) * K::kMBytes + h * 2 * kQ * kQ * 2, ml = mh + kQ * kQ * 2;
 #pragma unroll
                         for (int kk = 0; kk < kQ / 16; ++kk) {
                             const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
@@ -520,41 +530,133 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             mma_bf16_ts_if(d, xl, sdesc_sw128(mh + off, 16, 1024), idesc_bf16(128, 64 - 16 * kk, false), 1, issue);
                         }
                     }
-                    mma_commit_if(bar(kIDone), issue);
+                    mma_commit_if(bar(kIDone + (c & 1)), issue);
                 }
             }
             if (!ok) { // the MMAs in flight end before their memory is given back
                 mma_commit_if(bar(kDrain), issue);
                 mbar_wait_bounded(bar(kDrain), 0, kDefaultWaitLimit);
             }
+        } else if (warp >= 2) { // ---- M: the decay masks times C B^T, as operands; two warps
+            const int odd = lane & 1; // a thread has a row and every other group of 8 columns
+            const float D0 = p.D != nullptr ? __ldg(p.D + u.h0) : 0.f;
+            const float D1 = p.D != nullptr && u.nh > 1 ? __ldg(p.D + u.h0 + 1) : 0.f;
+            for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
+                const int gs = c % K::kGateSlots;
+                // 16-blocks of rows 0 and 3, or 1 and 2, columns up to the end of the row's block: (row, column)
+                // blocks (0, 0) (3, 0) (3, 1) (3, 2) (3, 3) of one warp, (1, 0) (1, 1) (2, 0) (2, 1) (2, 2) of the other
+                auto block_of = [&](int k, int &rb, int &i) {
+                    rb = warp == 2 ? (k == 0 ? 0 : 3) : (k < 2 ? 1 : 2);
+                    i = warp == 2 ? (k == 0 ? 0 : k - 1) : (k < 2 ? k : k - 2);
+                };
+                const float *cbc = a.cb + ((id0 + c) * p.G + u.g) * (kQ * kQ) + (lane >> 1) * kQ + 8 * odd;
+                auto load_cb = [&](int k, float (&v)[8]) {
+                    int rb, i;
+                    block_of(k, rb, i);
+                    const float4 *src = reinterpret_cast<const float4 *>(cbc + 16 * rb * kQ + 16 * i);
+                    *reinterpret_cast<float4 *>(v) = __ldg(src);
+                    *reinterpret_cast<float4 *>(v + 4) = __ldg(src + 1);
+                };
+                float v[8], next[8];
+                load_cb(0, v);
+                // I of two chunks ago has read this buffer
+                if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || (c > 1 && !wait_all(kIDone + (c & 1), ((c >> 1) & 1) ^ 1)))
+                    break;
+                const uint32_t mbuf = mbase + (c & 1) * K::kMBytes;
+#pragma unroll 1
+                for (int blk = 0; blk < 5; ++blk) {
+                    int rb, i;
+                    block_of(blk, rb, i);
+                    if (blk < 4)
+                        load_cb(blk + 1, next);
+                    const int t = 16 * rb + (lane >> 1), s0 = 16 * i + 8 * odd;
+#pragma unroll 1
+                    for (int h = 0; h < u.nh; ++h) {
+                        const float *rec = gate[gs][h];
+                        const float gh = rec[t], gl = rec[64 + t];
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 8; k += 4) {
+                            const float4 sh = *reinterpret_cast<const float4 *>(rec + s0 + k);
+                            const float4 sl = *reinterpret_cast<const float4 *>(rec + 64 + s0 + k);
+                            const float4 sd = *reinterpret_cast<const float4 *>(rec + 128 + s0 + k);
+                            float m[4];
+                            m[0] = ex2(kLog2e * ((gh - sh.x) + (gl - sl.x))) * sd.x * v[k];
+                            m[1] = ex2(kLog2e * ((gh - sh.y) + (gl - sl.y))) * sd.y * v[k + 1];
+                            m[2] = ex2(kLog2e * ((gh - sh.z) + (gl - sl.z))) * sd.z * v[k + 2];
+                            m[3] = ex2(kLog2e * ((gh - sh.w) + (gl - sl.w))) * sd.w * v[k + 3];
+                            if (i == rb) { // the diagonal block
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    if (s0 + k + j > t)
+                                        m[j] = 0.f;
+                                    if (s0 + k + j == t)
+                                        m[j] += h == 0 ? D0 : D1;
+                                }
+                            }
+                            split2(m[0], m[1], hi[k / 2], lo[k / 2]);
+                            split2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
+                        }
+                        // K-major rows of 128 bytes, 16-byte pieces swizzled by the row
+                        const uint32_t at = mbuf + h * 2 * kQ * kQ * 2 + t * 128 + (((s0 >> 3) ^ (t & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kQ * kQ * 2), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = next[k];
+                }
+                fence_proxy_async_smem();
+                arrive(kMFull + (c & 1));
+                arrive(kGEmpty + gs);
+            }
         }
-    } else if (wg == 1) { // ---- X: convolution of x, then x' and x as operands
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f, r[3] = {0.f, 0.f, 0.f};
+    } else if (wg < 3) { // ---- X: convolution of x, then x' and x as operands; 32 tokens of a chunk per warpgroup
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        const int half = wg - 1;
+        float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f, win[3] = {0.f, 0.f, 0.f};
         if (live) {
             const float4 w = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + chan);
             w0 = w.x; w1 = w.y; w2 = w.z; w3 = w.w;
             if (p.conv_b != nullptr)
                 wb = __ldg(p.conv_b + chan);
-            if (u.nc > 0) {
+            if (u.nc > 0 && half == 0) {
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     const T *src = conv_row<T>(p, u.n, u.start, u.start + u.c0 * kQ - 3 + i);
-                    r[i] = src != nullptr ? to_f(src[chan]) : 0.f;
+                    win[i] = src != nullptr ? to_f(src[chan]) : 0.f;
                 }
             }
         }
         for (int c = 0; c < u.nc; ++c) {
             const int64_t t0 = u.start + (u.c0 + c) * kQ;
-            const int ntok = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) : 0;
-            const T *src = reinterpret_cast<const T *>(p.xbc) + t0 * p.xbc_stride + chan;
-            float x[kQ];
+            const int ntok = (int)(u.end - t0 < kQ ? u.end - t0 : kQ), last = ntok - 1;
+            // a half without a head of its own reads the other's channels, and takes none of them
+            const T *src = reinterpret_cast<const T *>(p.xbc) + t0 * p.xbc_stride + (live ? chan : chan - 64);
+            float x[32], r[3];
+            {
+                // unconditional loads, the last token in the place of those behind it: all are in flight together
+                T raw[35];
 #pragma unroll
-            for (int t = 0; t < kQ; ++t)
-                x[t] = t < ntok ? to_f(src[t * p.xbc_stride]) : 0.f;
+                for (int t = 0; t < 35; ++t) {
+                    const int k = 32 * half + t - 3;
+                    raw[t] = src[(int64_t)(k < last ? k < 0 && c == 0 ? 0 : k : last) * p.xbc_stride];
+                }
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    r[t] = half == 0 && c == 0 ? win[t] : to_f(raw[t]);
+#pragma unroll
+                for (int t = 0; t < 32; ++t)
+                    x[t] = to_f(raw[t + 3]);
+            }
+            { // the next chunk's channels to L2, a 128-byte line per thread
+                const int t = kQ + (tid & 63), line = (tid >> 6) & 3;
+                if (t0 + t < u.end && line < (int)sizeof(T))
+                    prefetch_l2(src - row + line * (128 / sizeof(T)) + t * p.xbc_stride);
+            }
             float zero = 0.f;
 #pragma unroll
-            for (int t = 0; t < kQ; t += 2) {
+            for (int t = 0; t < 32; t += 2) {
                 const float ra = x[t], rb = x[t + 1];
                 x[t] = fmaf(w3, ra, fmaf(w2, r[2], fmaf(w1, r[1], fmaf(w0, r[0], wb))));
                 x[t + 1] = fmaf(w3, rb, fmaf(w2, ra, fmaf(w1, r[2], fmaf(w0, r[1], wb))));
@@ -562,30 +664,30 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 r[1] = ra;
                 r[2] = rb;
                 silu2(x[t], x[t + 1]);
-                if (t >= ntok)
+            }
+            const int valid = live ? ntok - 32 * half : 0;
+#pragma unroll
+            for (int t = 0; t < 32; ++t) {
+                if (t >= valid)
                     x[t] = 0.f;
-                if (t + 1 >= ntok)
-                    x[t + 1] = 0.f;
                 zero = fmaf(x[t], 0.f, zero);
-                zero = fmaf(x[t + 1], 0.f, zero);
             }
             const int gs = c % K::kGateSlots;
             if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || !wait_all(kUDone, (c & 1) ^ 1))
                 break;
             tc_fence_after();
+            const float4 *wt = reinterpret_cast<const float4 *>(gate[gs][hl] + 192 + 32 * half);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float4 *wt = reinterpret_cast<const float4 *>(gate[gs][hl] + 192 + 32 * half);
-                uint32_t hi[16], lo[16];
+            for (int t = 0; t < 32; t += 16) {
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float4 w = wt[k];
-                    const int t = 32 * half + 4 * k;
-                    split2(x[t] * w.x, x[t + 1] * w.y, hi[2 * k], lo[2 * k]);
-                    split2(x[t + 2] * w.z, x[t + 3] * w.w, hi[2 * k + 1], lo[2 * k + 1]);
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 w = wt[(t + k) / 4];
+                    split2(x[t + k] * w.x, x[t + k + 1] * w.y, hi[k / 2], lo[k / 2]);
+                    split2(x[t + k + 2] * w.z, x[t + k + 3] * w.w, hi[k / 2 + 1], lo[k / 2 + 1]);
                 }
-                tmem_st16(tmem + lanes + K::kXP + 16 * half, reinterpret_cast<const float(&)[16]>(hi));
-                tmem_st16(tmem + lanes + K::kXP + 32 + 16 * half, reinterpret_cast<const float(&)[16]>(lo));
+                tmem_st8(tmem + lanes + K::kXP + 16 * half + t / 2, hi);
+                tmem_st8(tmem + lanes + K::kXP + 32 + 16 * half + t / 2, lo);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -593,7 +695,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             arrive(kGEmpty + gs);
             if (SUMMARY)
                 continue;
-            if (!wait_all(kIDone, (c & 1) ^ 1))
+            if (c > 0 && !wait_all(kIDone + ((c - 1) & 1), ((c - 1) >> 1) & 1))
                 break;
             tc_fence_after();
             // A non-finite x would reach the tokens before it in its 16-block (as 0 times it): the
@@ -601,29 +703,29 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             int first = kQ;
             if (zero != 0.f) {
 #pragma unroll
-                for (int t = kQ - 1; t >= 0; --t)
+                for (int t = 31; t >= 0; --t)
                     if (!(fabsf(x[t]) <= 3.402823466e38f)) {
-                        first = t;
+                        first = 32 * half + t;
                         x[t] = 0.f;
                     }
             }
-            bad[c & 1][row] = first;
+            bad[c & 1][half][row] = first;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t hi[16], lo[16];
+            for (int t = 0; t < 32; t += 16) {
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    split2(x[32 * half + 2 * k], x[32 * half + 2 * k + 1], hi[k], lo[k]);
-                tmem_st16(tmem + lanes + K::kX + 16 * half, reinterpret_cast<const float(&)[16]>(hi));
-                tmem_st16(tmem + lanes + K::kX + 32 + 16 * half, reinterpret_cast<const float(&)[16]>(lo));
+                for (int k = 0; k < 8; ++k)
+                    split2(x[t + 2 * k], x[t + 2 * k + 1], hi[k], lo[k]);
+                tmem_st8(tmem + lanes + K::kX + 16 * half + t / 2, hi);
+                tmem_st8(tmem + lanes + K::kX + 32 + 16 * half + t / 2, lo);
             }
             tmem_wait_st();
             tc_fence_before();
             arrive(kXFull);
         }
-    } else if (wg < 4) { // ---- S: the state, CW columns of a row per thread
+    } else if (wg < 5) { // ---- S: the state, CW columns of a row per thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        const int half = wg - 2;
+        const int half = wg - 3;
         const int tiles = gridDim.x;
         float h[CW];
         auto seg_at = [&](int s) { // state `s` of this sequence and tile in the workspace
@@ -680,26 +782,27 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     break;
                 tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < CW; i += 32) {
-                    float v[32];
-                    tmem_ld32(tmem + lanes + K::kDH + CW * half + i, v);
+                for (int i = 0; i < CW; i += 16) {
+                    float v[2][8];
+                    tmem_ld8(tmem + lanes + K::kDH + CW * half + i, v[0]);
+                    tmem_ld8(tmem + lanes + K::kDH + CW * half + i + 8, v[1]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        h[i + k] = fmaf(gamma, h[i + k], v[k]);
+                    for (int k = 0; k < 16; ++k)
+                        h[i + k] = fmaf(gamma, h[i + k], v[k / 8][k % 8]);
                 }
             }
             if (c == u.nc)
                 break;
             if (!SUMMARY) {
 #pragma unroll
-                for (int i = 0; i < CW; i += 32) {
-                    uint32_t hi[16], lo[16];
+                for (int i = 0; i < CW; i += 16) {
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
+                    for (int k = 0; k < 8; ++k)
                         split2(h[i + 2 * k], h[i + 2 * k + 1], hi[k], lo[k]);
-                    tmem_st16(tmem + lanes + K::kDH + CW * half + i / 2, reinterpret_cast<const float(&)[16]>(hi));
-                    tmem_st16(tmem + lanes + K::kDH + CW * half + CW / 2 + i / 2, reinterpret_cast<const float(&)[16]>(lo));
+                    tmem_st8(tmem + lanes + K::kDH + CW * half + i / 2, hi);
+                    tmem_st8(tmem + lanes + K::kDH + CW * half + CW / 2 + i / 2, lo);
                 }
                 tmem_wait_st();
             }
@@ -713,99 +816,77 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         } else if (ok && u.seg == a.segments - 1 && live && p.final_state != nullptr) {
             store_state(p.final_state + gstate);
         }
-    } else if (wg == 4) { // ---- Y: the output
+    } else { // ---- Y: the output; 32 tokens of a chunk per warpgroup
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        const int half = wg - 5;
+        const int64_t ys = (int64_t)p.H * P;
         for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
             const int64_t t0 = u.start + (u.c0 + c) * kQ;
-            const int ntok = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) : 0;
+            const int ntok = (int)(u.end - t0 < kQ ? u.end - t0 : kQ), last = ntok - 1;
             const int gs = c % K::kGateSlots;
-            if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || !wait_all(kIDone, c & 1))
+            const T *zc = reinterpret_cast<const T *>(p.z) + t0 * p.z_stride + (live ? chan : chan - 64);
+            if (p.z != nullptr) { // the next chunk's gate inputs to L2, a 128-byte line per thread
+                const int t = kQ + (tid & 63), line = (tid >> 6) & 3;
+                if (t0 + t < u.end && line < (int)sizeof(T))
+                    prefetch_l2(zc - row + line * (128 / sizeof(T)) + t * p.z_stride);
+            }
+            T raw[8]; // z of 8 tokens, on its way while what comes before it is worked on
+            auto load_z = [&](int first) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    raw[t] = zc[(int64_t)(first + t < last ? first + t : last) * p.z_stride];
+            };
+            if (p.z != nullptr)
+                load_z(32 * half);
+            if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || !wait_all(kIDone + (c & 1), (c >> 1) & 1))
                 break;
             tc_fence_after();
-            float y[kQ];
-#pragma unroll
-            for (int t = 0; t < kQ; t += 16) {
-                float v[16];
-                float e[16];
-                tmem_ld16(tmem + lanes + K::kYI + t, v);
-                tmem_ld16(tmem + lanes + K::kYA + 64 * hl + t, e);
+            int nf = bad[c & 1][0][row];
+            if (half == 1)
+                nf = min(nf, bad[c & 1][1][row]);
+#pragma unroll 1
+            for (int first = 32 * half; first < 32 * half + 32; first += 8) {
+                float y[8], e[8];
+                tmem_ld8(tmem + lanes + K::kYI + first, y);
+                tmem_ld8(tmem + lanes + K::kYA + 64 * hl + first, e);
                 tmem_wait_ld();
-                const float4 *eg = reinterpret_cast<const float4 *>(gate[gs][hl] + 256 + t);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 f = eg[k];
-                    y[t + 4 * k] = fmaf(f.x, v[4 * k], e[4 * k]);
-                    y[t + 4 * k + 1] = fmaf(f.y, v[4 * k + 1], e[4 * k + 1]);
-                    y[t + 4 * k + 2] = fmaf(f.z, v[4 * k + 2], e[4 * k + 2]);
-                    y[t + 4 * k + 3] = fmaf(f.w, v[4 * k + 3], e[4 * k + 3]);
+                for (int k = 0; k < 8; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(gate[gs][hl] + 256 + first + k);
+                    y[k] = fmaf(f.x, y[k], e[k]);
+                    y[k + 1] = fmaf(f.y, y[k + 1], e[k + 1]);
+                    y[k + 2] = fmaf(f.z, y[k + 2], e[k + 2]);
+                    y[k + 3] = fmaf(f.w, y[k + 3], e[k + 3]);
                 }
-            }
-            const int first = bad[c & 1][row];
-            tc_fence_before();
-            arrive(kYEmpty);
-            arrive(kGEmpty + gs);
-            if (first < kQ) {
-#pragma unroll
-                for (int t = 0; t < kQ; ++t)
-                    if (t >= first)
-                        y[t] = __uint_as_float(0x7fffffffu);
-            }
-            T *dst = reinterpret_cast<T *>(p.y) + t0 * p.H * P + chan;
-            const int64_t ys = (int64_t)p.H * P;
-            if (p.z != nullptr) {
-                const T *z = reinterpret_cast<const T *>(p.z) + t0 * p.z_stride + chan;
-#pragma unroll
-                for (int t = 0; t < kQ; t += 2) {
-                    float za = t < ntok ? to_f(z[t * p.z_stride]) : 0.f, zb = t + 1 < ntok ? to_f(z[(t + 1) * p.z_stride]) : 0.f;
-                    silu2(za, zb);
-                    y[t] *= za;
-                    y[t + 1] *= zb;
+                if (first == 32 * half + 24) {
+                    tc_fence_before();
+                    arrive(kYEmpty);
+                    arrive(kGEmpty + gs);
                 }
-            }
+                if (p.z != nullptr) {
 #pragma unroll
-            for (int t = 0; t < kQ; ++t)
-                if (t < ntok)
-                    dst[t * ys] = from_f<T>(y[t]);
-        }
-    } else { // ---- M: the decay masks times C B^T, as operands
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        const int t = 16 * q + (lane >> 1), odd = lane & 1; // a row and every other group of 8 columns
-        for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
-            const int gs = c % K::kGateSlots;
-            if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || !wait_all(kIDone, (c & 1) ^ 1))
-                break;
-            const float *row_cb = a.cb + ((id0 + c) * p.G + u.g) * (kQ * kQ) + t * kQ;
-            for (int i = 0; i <= q; ++i) { // columns up to the end of the row's 16-block
-                const int s0 = 16 * i + 8 * odd;
-                float v[8];
-                *reinterpret_cast<float4 *>(v) = __ldg(reinterpret_cast<const float4 *>(row_cb + s0));
-                *reinterpret_cast<float4 *>(v + 4) = __ldg(reinterpret_cast<const float4 *>(row_cb + s0 + 4));
-                for (int h = 0; h < u.nh; ++h) {
-                    const float *rec = gate[gs][h];
-                    const float gh = rec[t], gl = rec[64 + t];
-                    const float Dh = p.D != nullptr ? __ldg(p.D + u.h0 + h) : 0.f;
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 8; k += 2) {
-                        float m[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int s = s0 + k + j;
-                            const float d = (gh - rec[s]) + (gl - rec[64 + s]);
-                            m[j] = s <= t ? ex2(kLog2e * d) * rec[128 + s] * v[k + j] : 0.f;
-                            if (s == t)
-                                m[j] += Dh;
-                        }
-                        split2(m[0], m[1], hi[k / 2], lo[k / 2]);
+                    for (int t = 0; t < 8; t += 2) {
+                        float za = to_f(raw[t]), zb = to_f(raw[t + 1]);
+                        silu2(za, zb);
+                        y[t] *= za;
+                        y[t + 1] *= zb;
                     }
-                    // K-major rows of 128 bytes, 16-byte pieces swizzled by the row
-                    const uint32_t at = mbase + h * 2 * kQ * kQ * 2 + t * 128 + (((s0 >> 3) ^ (t & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kQ * kQ * 2), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+                    if (first < 32 * half + 24)
+                        load_z(first + 8);
                 }
+                if (nf < first + 8) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        if (first + t >= nf)
+                            y[t] = __uint_as_float(0x7fffffffu);
+                }
+                T *dst = reinterpret_cast<T *>(p.y) + (t0 + first) * ys + chan;
+                const int valid = live ? ntok - first : 0;
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    if (t < valid)
+                        dst[t * ys] = from_f<T>(y[t]);
             }
-            fence_proxy_async_smem();
-            arrive(kMFull);
-            arrive(kGEmpty + gs);
         }
     }
     __syncwarp();
