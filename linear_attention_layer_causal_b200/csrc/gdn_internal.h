@@ -153,10 +153,10 @@ struct SsmArgs {
     void *conv_cache = nullptr;  // decode: resident windows
     const float *conv_w, *conv_b, *A_log, *dt_bias, *D;
     void *ws = nullptr;
-    int segments = 1;            // prefill: segments per sequence
+    int segments = 1, fine = 1;  // prefill: segments per sequence, parts of each in the summary pass
     constexpr int conv_dim() const { return H * P + 2 * G * S; }
 };
-int ssm_segments(const gdn_ssm_config *c, int batch, int64_t N); // the call's own, or the library's choice
+void ssm_cut(const gdn_ssm_config *c, int batch, int64_t N, int *segments, int *fine);
 bool ssm_addressable(const gdn_ssm_config *c, int batch, int64_t N);
 size_t ssm_workspace_bytes(const gdn_ssm_config *c, int batch, int64_t N);
 cudaError_t launch_ssm_prefill(const SsmArgs &p, cudaEvent_t begin, cudaEvent_t end, cudaStream_t s);

@@ -138,7 +138,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *para
     p.final_state = final_state;
     p.final_conv = final_conv;
     p.ws = workspace;
-    p.segments = ssm_segments(cfg, batch, total_tokens);
+    ssm_cut(cfg, batch, total_tokens, &p.segments, &p.fine);
     return cuda_status(launch_ssm_prefill(p, hook.begin, hook.end, (cudaStream_t)stream));
 }
 

@@ -31,7 +31,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kQ = 64;        // tokens of a chunk
-constexpr int kGateRec = 320; // floats of a (chunk, head): G, its low part, delta, x' weight, e^G
+constexpr int kGateRec = 320; // floats of a (chunk, head): G / ln 2, its low part, delta, x' weight, e^G
 constexpr int kSMs = 148;
 constexpr uint32_t kStatusTimeout = 1u;
 
@@ -46,7 +46,7 @@ int64_t max_chunks(int64_t N, int batch) { return N / kQ + batch; }
 struct Layout { // workspace offsets in bytes
     size_t bc, cb, gates, seg, segdecay, total;
 };
-Layout layout(int G, int H, int P, int S, int64_t N, int batch, int segments) {
+Layout layout(int G, int H, int P, int S, int64_t N, int batch, int slots) {
     const size_t chunks = (size_t)max_chunks(N, batch);
     const size_t tiles = (size_t)G * (((size_t)(H / G) * P + 127) / 128);
     Layout l;
@@ -54,8 +54,8 @@ Layout layout(int G, int H, int P, int S, int64_t N, int batch, int segments) {
     l.cb = l.bc + round_up(chunks * G * kQ * 4 * S * 2);
     l.gates = l.cb + round_up(chunks * G * kQ * kQ * 4);
     l.seg = l.gates + round_up(chunks * H * kGateRec * 4);
-    l.segdecay = l.seg + (segments > 1 ? round_up((size_t)batch * tiles * segments * 128 * S * 4) : 0);
-    l.total = l.segdecay + (segments > 1 ? round_up((size_t)batch * tiles * segments * 2 * 4) : 0);
+    l.segdecay = l.seg + (slots > 1 ? round_up((size_t)batch * tiles * slots * 128 * S * 4) : 0);
+    l.total = l.segdecay + (slots > 1 ? round_up((size_t)batch * tiles * slots * 2 * 4) : 0);
     return l;
 }
 
@@ -99,8 +99,6 @@ template <typename T> __device__ __forceinline__ const T *conv_row(const SsmArgs
         return nullptr;
     return reinterpret_cast<const T *>(p.init_conv) + ((int64_t)n * 3 + 3 + (t - start)) * p.conv_dim();
 }
-
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------------- prep
 
@@ -237,12 +235,13 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const double G = before + s[i];
-            const float gh = (float)G;
+            const double G2 = G * 1.4426950408889634; // for base-2 exponentials
+            const float gh = (float)G2;
             rec[i] = gh;
-            rec[64 + i] = (float)(G - (double)gh);
+            rec[64 + i] = (float)(G2 - (double)gh);
             rec[128 + i] = d[i];
             rec[192 + i] = d[i] == 0.f ? 0.f : d[i] * expf((float)(all - G));
-            rec[256 + i] = expf(gh);
+            rec[256 + i] = expf((float)G);
         }
     }
     __syncthreads();
@@ -307,12 +306,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-                 : "r"(taddr)
-                 : "memory");
-}
 // Untiled bulk copy of `bytes` (a multiple of 16, both ends 16-byte aligned).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -320,13 +313,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-template <int P, int S> struct Scan {
-    static constexpr int kHeads = 128 / P;      // of a block
-    static constexpr int kStages = 2;           // chunks of B and C in shared memory
+template <typename T, int P, int S> struct Scan {
+    static constexpr int kHeads = 128 / P;            // of a block
+    static constexpr int kCW = S / 4;                 // state columns of an S warpgroup
+    static constexpr int kHalf = 2 * S * kQ * 2;      // bytes of a chunk's B (or C): hi, lo
+    static constexpr int kSlots = 3;                  // of them in shared memory: C, B, C, B, ... in turn
     static constexpr int kGateSlots = 4;
-    static constexpr int kStageBytes = 4 * S * kQ * 2;
-    static constexpr int kMBytes = kHeads * 2 * kQ * kQ * 2; // M hi, lo of each head; two buffers
-    static constexpr size_t kSmem = 1024 + kStages * kStageBytes + 2 * kMBytes;
+    static constexpr int kMBytes = kHeads * 2 * kQ * kQ * 2; // M hi, lo of each head
+    static constexpr int kMBufs = sizeof(T) == 2 ? 2 : 1;
+    static constexpr int kCbBytes = kQ * kQ * 4;
+    static constexpr int kRow = 128 * sizeof(T);      // 128 channels of a token
+    static constexpr int kXBytes = (kQ + 3) * kRow, kZBytes = kQ * kRow;
+    static constexpr int kOffM = kSlots * kHalf, kOffCb = kOffM + kMBufs * kMBytes, kOffX = kOffCb + kCbBytes,
+                         kOffZ = kOffX + kXBytes;
+    static constexpr size_t kSmem = 1024 + kOffZ + kZBytes;
     // TMEM columns
     static constexpr uint32_t kDH = 0;             // x' B^T, then H hi and lo of the next chunk
     static constexpr uint32_t kYI = 128;           // H C^T
@@ -334,11 +334,14 @@ template <int P, int S> struct Scan {
     static constexpr uint32_t kXP = 320;           // x' hi, lo
     static constexpr uint32_t kX = 384;            // x hi, lo
 };
-constexpr int kScanThreads = 896;
+constexpr int kScanThreads = 1024;
 constexpr uint32_t kTmemCols = 512;
 
-// pairs (by the chunk's parity), the gate slots, and single barriers
-enum Bar { kBcFull = 0, kBcEmpty = 2, kMFull = 4, kIDone = 6, kGFull = 8, kGEmpty = 12, kXpFull = 16, kXFull, kHFull, kUDone, kYEmpty, kDrain, kBars };
+// B and C slots, M buffers, gate slots, and single barriers
+enum Bar {
+    kBcFull = 0, kBcEmpty = 3, kMFull = 6, kIDone = 8, kGFull = 10, kGEmpty = 14,
+    kXpFull = 18, kXFull, kHFull, kUDone, kYEmpty, kCbFull, kCbEmpty, kDrain, kBars
+};
 
 // What a block works on.
 struct Unit {
@@ -370,48 +373,57 @@ struct ScanArgs {
     const float *cb, *gates;
     float *seg, *segdecay;
     uint32_t *status;
-    int segments, tiles_per_group;
+    int segments, fine, tiles_per_group; // the summary pass cuts every segment into `fine`
 };
 
+// The `n` threads of some warpgroups (named barrier `id`).
+__device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Warpgroups: 0 loads, MMAs and M (two warps); 1, 2 X (32 tokens of a chunk
+// each); 3 to 6 S (a quarter of the state's columns each); 7 Y.
 // SUMMARY: only the states of the segments but the last, from zero (the first
 // from the initial state, which is also copied); no output.
 template <typename T, int P, int S, bool SUMMARY>
 __global__ void __launch_bounds__(kScanThreads, 1)
-    ssm_scan_kernel(const __grid_constant__ CUtensorMap tbc, const ScanArgs a) {
-    using K = Scan<P, S>;
-    constexpr int NH = K::kHeads, CW = S / 2; // state columns of an S warpgroup
+    ssm_scan_kernel(const __grid_constant__ CUtensorMap tbc, const __grid_constant__ CUtensorMap tcb, const ScanArgs a) {
+    using K = Scan<T, P, S>;
+    constexpr int NH = K::kHeads, CW = K::kCW;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ __align__(16) float gate[K::kGateSlots][NH][kGateRec];
-    __shared__ int bad[2][2][128]; // per half of a chunk and row: the first token with a non-finite x
+    __shared__ uint8_t bad[2][2][128]; // per half of a chunk and row: the first token with a non-finite x
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t mbase = base + K::kStages * K::kStageBytes;
+    const uint8_t *sm = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t b0 = smem_u32(bars);
     auto bar = [&](int i) { return b0 + 8u * i; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, wg = warp >> 2;
     const SsmArgs &p = a.p;
-    const Unit u = unit_of<P>(p, a.segments, a.tiles_per_group);
+    const Unit u = unit_of<P>(p, SUMMARY ? a.segments * a.fine : a.segments, a.tiles_per_group);
     const int64_t id0 = first_chunk(u.start, u.n) + u.c0;
     volatile uint32_t *abort_v = &abort_flag;
 
     if (tid == 0) {
-        const int consumers = SUMMARY ? 16 : 26;
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < K::kSlots; ++i) {
             mbar_init(bar(kBcFull + i), 1);
             mbar_init(bar(kBcEmpty + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kMFull + i), 2);
             mbar_init(bar(kIDone + i), 1);
         }
         for (int i = 0; i < K::kGateSlots; ++i) {
             mbar_init(bar(kGFull + i), 1);
-            mbar_init(bar(kGEmpty + i), consumers);
+            mbar_init(bar(kGEmpty + i), SUMMARY ? 24 : 30); // X 8, S 16, Y 4 and M 2 warps
         }
         mbar_init(bar(kXpFull), 8);
         mbar_init(bar(kXFull), 8);
-        mbar_init(bar(kHFull), 8);
+        mbar_init(bar(kHFull), 16);
         mbar_init(bar(kUDone), 1);
-        mbar_init(bar(kYEmpty), 8);
+        mbar_init(bar(kYEmpty), 4);
+        mbar_init(bar(kCbFull), 1);
+        mbar_init(bar(kCbEmpty), 2);
         mbar_init(bar(kDrain), 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -439,56 +451,107 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         if (lane == 0)
             mbar_arrive(bar(i));
     };
+    auto gate_ready = [&](int c) { return wait_all(kGFull + c % K::kGateSlots, (c / K::kGateSlots) & 1); };
+    auto i_done = [&](int c) { return wait_all(kIDone + (c & 1), (c >> 1) & 1); };
     const int row = 32 * q + lane;          // state row of a thread of the X, S, Y warpgroups
     const int hl = P == 64 ? q >> 1 : 0;    // its head within the block (uniform over the warp)
     const bool live = hl < u.nh;
     const int64_t chan = (int64_t)u.h0 * P + row; // its x channel
+    // Copies of 128 channels (those of absent heads left out) of the tokens first .. kQ - 1 of a chunk to shared
+    // memory, by n threads; a token behind the end of the sequence is the last one instead.
+    auto copy_rows = [&](uint32_t dst, const void *src, int64_t stride, int64_t t0, int c, int first, int me, int n) {
+        constexpr int PIECES = K::kRow / 16;
+        const int last = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 1;
+        const int pieces = u.nh * (P * (int)sizeof(T) / 16);
+        for (int i = me; i < (kQ - first) * PIECES; i += n) {
+            const int t = first + i / PIECES, k = i % PIECES;
+            const T *at = reinterpret_cast<const T *>(src) + (t0 + (t < last ? t : last)) * stride;
+            bool zeros = false;
+            if (t < 0 && c == 0) { // before the segment: the window, or the rows of the segment ahead
+                const T *row_before = conv_row<T>(p, u.n, u.start, t0 + t);
+                zeros = row_before == nullptr;
+                at = zeros ? reinterpret_cast<const T *>(src) : row_before;
+            }
+            if (k < pieces)
+                cp_async16(dst + (t - first) * K::kRow + 16 * k, at + u.h0 * P + k * (16 / (int)sizeof(T)), zeros);
+        }
+    };
 
     if (wg == 0) {
-        // 128 x (64 + 2 x 64 + 2 x 104 + 2 x 48) registers, of 896 x 72 that the block was launched with
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == 0 && lane == 0) { // ---- loads
-            const int gbytes = u.nh * kGateRec * 4;
-            int c = 0;
-            for (; c < u.nc; ++c) {
-                const int s = c & 1, gs = c % K::kGateSlots;
-                if (!wait(kGEmpty + gs, ((c / K::kGateSlots) & 1) ^ 1))
-                    break;
-                mbar_arrive_expect_tx(bar(kGFull + gs), gbytes);
-                bulk_load(smem_u32(gate[gs]), a.gates + ((id0 + c) * p.H + u.h0) * kGateRec, gbytes, bar(kGFull + gs));
-                if (!wait(kBcEmpty + s, ((c >> 1) & 1) ^ 1)) {
-                    mbar_wait_bounded(bar(kGFull + gs), (c / K::kGateSlots) & 1, kDefaultWaitLimit);
-                    break;
+        // 128 x (56 + 2 x 64 + 4 x 56 + 96) registers, of 1024 x 64 that the block was launched with
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            if (lane == 0) { // ---- loads
+                const int gbytes = u.nh * kGateRec * 4;
+                // slots of B and C in the order of their use: C B C B ..., or B B ... in the summary
+                int slot = 0, used = 0;
+                uint32_t ph = 1;
+                bool ok = true;
+                for (int c = 0; ok && c < u.nc; ++c) {
+                    const int gs = c % K::kGateSlots;
+                    if (!(ok = wait(kGEmpty + gs, ((c / K::kGateSlots) & 1) ^ 1)))
+                        break;
+                    mbar_arrive_expect_tx(bar(kGFull + gs), gbytes);
+                    bulk_load(smem_u32(gate[gs]), a.gates + ((id0 + c) * p.H + u.h0) * kGateRec, gbytes, bar(kGFull + gs));
+                    const int y = (int)(((id0 + c) * p.G + u.g) * kQ);
+                    if (!SUMMARY) {
+                        if (!(ok = wait(kCbEmpty, (c & 1) ^ 1))) {
+                            mbar_wait_bounded(bar(kGFull + gs), (c / K::kGateSlots) & 1, kDefaultWaitLimit);
+                            break;
+                        }
+                        mbar_arrive_expect_tx(bar(kCbFull), K::kCbBytes);
+                        tma_load_2d(base + K::kOffCb, &tcb, 0, y, bar(kCbFull));
+                        tma_load_2d(base + K::kOffCb + 8192, &tcb, 32, y, bar(kCbFull));
+                    }
+                    for (int part = SUMMARY ? 1 : 0; part < 2; ++part) { // C (channels 2 S ..), then B
+                        if (!(ok = wait(kBcEmpty + slot, ph))) {
+                            mbar_wait_bounded(bar(kGFull + gs), (c / K::kGateSlots) & 1, kDefaultWaitLimit);
+                            if (!SUMMARY)
+                                mbar_wait_bounded(bar(kCbFull), c & 1, kDefaultWaitLimit);
+                            break;
+                        }
+                        mbar_arrive_expect_tx(bar(kBcFull + slot), K::kHalf);
+                        for (int k = 0; k < 2 * S / 64; ++k) // boxes of 64 channels: hi, lo
+                            tma_load_2d(base + slot * K::kHalf + k * 8192, &tbc, 64 * k + (part == 0 ? 2 * S : 0), y,
+                                        bar(kBcFull + slot));
+                        used = used < K::kSlots ? used + 1 : K::kSlots;
+                        if (++slot == K::kSlots) {
+                            slot = 0;
+                            ph ^= 1;
+                        }
+                    }
                 }
-                // boxes of 64 channels: B hi, B lo, C hi, C lo
-                constexpr int BOXES = (SUMMARY ? 2 : 4) * S / 64;
-                mbar_arrive_expect_tx(bar(kBcFull + s), BOXES * 8192);
-                const int y = (int)(((id0 + c) * p.G + u.g) * kQ);
-                for (int k = 0; k < BOXES; ++k)
-                    tma_load_2d(base + s * K::kStageBytes + k * 8192, &tbc, 64 * k, y, bar(kBcFull + s));
-            }
-            if (c < u.nc) { // gave up: the copies in flight land before the block may end
-                for (int k = c - 1; k >= 0 && k >= c - 4; --k) {
-                    mbar_wait_bounded(bar(kGFull + k % K::kGateSlots), (k / K::kGateSlots) & 1, kDefaultWaitLimit);
-                    if (k >= c - 2)
-                        mbar_wait_bounded(bar(kBcFull + (k & 1)), (k >> 1) & 1, kDefaultWaitLimit);
+                if (!ok) { // gave up: the copies in flight land before the block may end
+                    for (int k = 0; k < used; ++k) {
+                        if (--slot < 0) {
+                            slot = K::kSlots - 1;
+                            ph ^= 1;
+                        }
+                        mbar_wait_bounded(bar(kBcFull + slot), ph ^ 1, kDefaultWaitLimit);
+                    }
                 }
             }
         } else if (warp == 1) { // ---- MMAs
             const uint32_t issue = elect_one();
             bool ok = true;
+            int slot = 0;
+            uint32_t sph = 0;
+            auto next_slot = [&]() {
+                if (++slot == K::kSlots) {
+                    slot = 0;
+                    sph ^= 1;
+                }
+            };
             for (int c = 0; c < u.nc; ++c) {
-                const uint32_t st = base + (c & 1) * K::kStageBytes;
-                const uint32_t bh = st, bl = st + S * 128, ch = st + 2 * S * 128, cl = st + 3 * S * 128;
                 const uint32_t ph = c & 1;
-                ok = wait_all(kBcFull + (c & 1), (c >> 1) & 1) && wait_all(kHFull, ph);
                 if (!SUMMARY) {
-                    ok = ok && wait_all(kYEmpty, ph ^ 1);
+                    ok = wait_all(kBcFull + slot, sph) && wait_all(kHFull, ph) && wait_all(kYEmpty, ph ^ 1);
                     if (!ok)
                         break;
                     tc_fence_after();
                     // Y: D[row][t] = sum_s H[row][s] C[t][s].  H hi of 16 columns kk sits beside lo in the
-                    // half of DH that its S warpgroup owns.
+                    // quarter of DH that its S warpgroup owns.
+                    const uint32_t ch = base + slot * K::kHalf, cl = ch + S * 128;
 #pragma unroll
                     for (int kk = 0; kk < S / 16; ++kk) {
                         const uint32_t hh = tmem + K::kDH + kk / (CW / 16) * CW + kk % (CW / 16) * 8, hlo = hh + CW / 2;
@@ -497,12 +560,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         mma_bf16_ts_if(tmem + K::kYI, hh, sdesc_sw128(cl + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
                         mma_bf16_ts_if(tmem + K::kYI, hlo, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
                     }
+                    mma_commit_if(bar(kBcEmpty + slot), issue);
+                    next_slot();
                 }
-                ok = ok && wait_all(kXpFull, ph);
+                ok = wait_all(kBcFull + slot, sph) && (!SUMMARY || wait_all(kHFull, ph)) && wait_all(kXpFull, ph);
                 if (!ok)
                     break;
                 tc_fence_after();
                 // U: D[row][s] = sum_t x'[row][t] B[t][s], over H once the MMAs above have read it
+                const uint32_t bh = base + slot * K::kHalf, bl = bh + S * 128;
 #pragma unroll
                 for (int kk = 0; kk < kQ / 16; ++kk) {
                     const uint32_t xh = tmem + K::kXP + 8 * kk, xl = xh + 32;
@@ -510,17 +576,20 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     mma_bf16_ts_if(tmem + K::kDH, xh, sdesc_sw128(bl + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
                     mma_bf16_ts_if(tmem + K::kDH, xl, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
                 }
-                mma_commit_if(bar(kBcEmpty + (c & 1)), issue);
                 mma_commit_if(bar(kUDone), issue);
+                mma_commit_if(bar(kBcEmpty + slot), issue);
+                next_slot();
                 if (!SUMMARY) {
-                    ok = wait_all(kXFull, ph) && wait_all(kMFull + (c & 1), (c >> 1) & 1);
+                    const int mb = c % K::kMBufs;
+                    ok = wait_all(kXFull, ph) && wait_all(kMFull + mb, (c / K::kMBufs) & 1);
                     if (!ok)
                         break;
                     tc_fence_after();
                     // I: D[row][t] = sum_{s <= t} x[row][s] M[t][s] for each head's M; all 128 rows take part, a
                     // head's rows read their own.  Tokens before a 16-block of s take nothing from it.
+#pragma unroll 1
                     for (int h = 0; h < u.nh; ++h) {
-                        const uint32_t mh = mbase + (c & 1) * K::kMBytes + h * 2 * kQ * kQ * 2, ml = mh + kQ * kQ * 2;
+                        const uint32_t mh = base + K::kOffM + mb * K::kMBytes + h * 2 * kQ * kQ * 2, ml = mh + kQ * kQ * 2;
 #pragma unroll
                         for (int kk = 0; kk < kQ / 16; ++kk) {
                             const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
@@ -537,39 +606,29 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 mma_commit_if(bar(kDrain), issue);
                 mbar_wait_bounded(bar(kDrain), 0, kDefaultWaitLimit);
             }
-        } else if (warp >= 2) { // ---- M: the decay masks times C B^T, as operands; two warps
+        } else { // ---- M: the decay masks times C B^T, as operands; two warps
             const int odd = lane & 1; // a thread has a row and every other group of 8 columns
             const float D0 = p.D != nullptr ? __ldg(p.D + u.h0) : 0.f;
             const float D1 = p.D != nullptr && u.nh > 1 ? __ldg(p.D + u.h0 + 1) : 0.f;
             for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
-                const int gs = c % K::kGateSlots;
-                // 16-blocks of rows 0 and 3, or 1 and 2, columns up to the end of the row's block: (row, column)
-                // blocks (0, 0) (3, 0) (3, 1) (3, 2) (3, 3) of one warp, (1, 0) (1, 1) (2, 0) (2, 1) (2, 2) of the other
-                auto block_of = [&](int k, int &rb, int &i) {
-                    rb = warp == 2 ? (k == 0 ? 0 : 3) : (k < 2 ? 1 : 2);
-                    i = warp == 2 ? (k == 0 ? 0 : k - 1) : (k < 2 ? k : k - 2);
-                };
-                const float *cbc = a.cb + ((id0 + c) * p.G + u.g) * (kQ * kQ) + (lane >> 1) * kQ + 8 * odd;
-                auto load_cb = [&](int k, float (&v)[8]) {
-                    int rb, i;
-                    block_of(k, rb, i);
-                    const float4 *src = reinterpret_cast<const float4 *>(cbc + 16 * rb * kQ + 16 * i);
-                    *reinterpret_cast<float4 *>(v) = __ldg(src);
-                    *reinterpret_cast<float4 *>(v + 4) = __ldg(src + 1);
-                };
-                float v[8], next[8];
-                load_cb(0, v);
-                // I of two chunks ago has read this buffer
-                if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || (c > 1 && !wait_all(kIDone + (c & 1), ((c >> 1) & 1) ^ 1)))
+                const int mb = c % K::kMBufs, gs = c % K::kGateSlots;
+                // the chunk that last had this buffer: its products are done
+                if (!gate_ready(c) || !wait_all(kCbFull, c & 1) || (c >= K::kMBufs && !i_done(c - K::kMBufs)))
                     break;
-                const uint32_t mbuf = mbase + (c & 1) * K::kMBytes;
+                const uint32_t mbuf = base + K::kOffM + mb * K::kMBytes;
+                // 16-blocks (row, column): (0, 0) (3, 0) (3, 1) (3, 2) (3, 3) of one warp, (1, 0) (1, 1) (2, 0)
+                // (2, 1) (2, 2) of the other
 #pragma unroll 1
                 for (int blk = 0; blk < 5; ++blk) {
-                    int rb, i;
-                    block_of(blk, rb, i);
-                    if (blk < 4)
-                        load_cb(blk + 1, next);
+                    const int rb = warp == 2 ? (blk == 0 ? 0 : 3) : (blk < 2 ? 1 : 2);
+                    const int i = warp == 2 ? (blk == 0 ? 0 : blk - 1) : (blk < 2 ? blk : blk - 2);
                     const int t = 16 * rb + (lane >> 1), s0 = 16 * i + 8 * odd;
+                    // two boxes of 32 columns, 16-byte pieces swizzled by the row
+                    const uint8_t *cbr = sm + K::kOffCb + (s0 >> 5) * 8192 + t * 128;
+                    const int piece = (s0 & 31) >> 2;
+                    float v[8];
+                    *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(cbr + ((piece ^ (t & 7)) << 4));
+                    *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(cbr + (((piece + 1) ^ (t & 7)) << 4));
 #pragma unroll 1
                     for (int h = 0; h < u.nh; ++h) {
                         const float *rec = gate[gs][h];
@@ -581,10 +640,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             const float4 sl = *reinterpret_cast<const float4 *>(rec + 64 + s0 + k);
                             const float4 sd = *reinterpret_cast<const float4 *>(rec + 128 + s0 + k);
                             float m[4];
-                            m[0] = ex2(kLog2e * ((gh - sh.x) + (gl - sl.x))) * sd.x * v[k];
-                            m[1] = ex2(kLog2e * ((gh - sh.y) + (gl - sl.y))) * sd.y * v[k + 1];
-                            m[2] = ex2(kLog2e * ((gh - sh.z) + (gl - sl.z))) * sd.z * v[k + 2];
-                            m[3] = ex2(kLog2e * ((gh - sh.w) + (gl - sl.w))) * sd.w * v[k + 3];
+                            m[0] = ex2((gh - sh.x) + (gl - sl.x)) * (sd.x * v[k]);
+                            m[1] = ex2((gh - sh.y) + (gl - sl.y)) * (sd.y * v[k + 1]);
+                            m[2] = ex2((gh - sh.z) + (gl - sl.z)) * (sd.z * v[k + 2]);
+                            m[3] = ex2((gh - sh.w) + (gl - sl.w)) * (sd.w * v[k + 3]);
                             if (i == rb) { // the diagonal block
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
@@ -602,58 +661,44 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kQ * kQ * 2), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
                     }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = next[k];
                 }
                 fence_proxy_async_smem();
-                arrive(kMFull + (c & 1));
+                arrive(kMFull + mb);
+                arrive(kCbEmpty);
                 arrive(kGEmpty + gs);
             }
         }
     } else if (wg < 3) { // ---- X: convolution of x, then x' and x as operands; 32 tokens of a chunk per warpgroup
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        const int half = wg - 1;
-        float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f, win[3] = {0.f, 0.f, 0.f};
+        const int half = wg - 1, me = tid - 128;
+        const uint32_t xbuf = base + K::kOffX;
+        float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f;
         if (live) {
             const float4 w = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + chan);
             w0 = w.x; w1 = w.y; w2 = w.z; w3 = w.w;
             if (p.conv_b != nullptr)
                 wb = __ldg(p.conv_b + chan);
-            if (u.nc > 0 && half == 0) {
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const T *src = conv_row<T>(p, u.n, u.start, u.start + u.c0 * kQ - 3 + i);
-                    win[i] = src != nullptr ? to_f(src[chan]) : 0.f;
-                }
-            }
         }
+        const int64_t tok0 = u.start + u.c0 * kQ;
+        bool ok = true;
+        if (u.nc > 0)
+            copy_rows(xbuf, p.xbc, p.xbc_stride, tok0, 0, -3, me, 256);
         for (int c = 0; c < u.nc; ++c) {
-            const int64_t t0 = u.start + (u.c0 + c) * kQ;
-            const int ntok = (int)(u.end - t0 < kQ ? u.end - t0 : kQ), last = ntok - 1;
-            // a half without a head of its own reads the other's channels, and takes none of them
-            const T *src = reinterpret_cast<const T *>(p.xbc) + t0 * p.xbc_stride + (live ? chan : chan - 64);
+            const int64_t t0 = tok0 + c * kQ;
+            cp_async_wait();
+            group_sync(1, 256); // every thread's copies have landed
             float x[32], r[3];
             {
-                // unconditional loads, the last token in the place of those behind it: all are in flight together
-                T raw[35];
-#pragma unroll
-                for (int t = 0; t < 35; ++t) {
-                    const int k = 32 * half + t - 3;
-                    raw[t] = src[(int64_t)(k < last ? k < 0 && c == 0 ? 0 : k : last) * p.xbc_stride];
-                }
+                const T *src = reinterpret_cast<const T *>(sm + K::kOffX) + (32 * half) * 128 + row;
 #pragma unroll
                 for (int t = 0; t < 3; ++t)
-                    r[t] = half == 0 && c == 0 ? win[t] : to_f(raw[t]);
+                    r[t] = to_f(src[t * 128]);
 #pragma unroll
                 for (int t = 0; t < 32; ++t)
-                    x[t] = to_f(raw[t + 3]);
+                    x[t] = to_f(src[(t + 3) * 128]);
             }
-            { // the next chunk's channels to L2, a 128-byte line per thread
-                const int t = kQ + (tid & 63), line = (tid >> 6) & 3;
-                if (t0 + t < u.end && line < (int)sizeof(T))
-                    prefetch_l2(src - row + line * (128 / sizeof(T)) + t * p.xbc_stride);
-            }
+            group_sync(1, 256); // every thread has its tokens
+            if (c + 1 < u.nc)
+                copy_rows(xbuf, p.xbc, p.xbc_stride, t0 + kQ, c + 1, -3, me, 256);
             float zero = 0.f;
 #pragma unroll
             for (int t = 0; t < 32; t += 2) {
@@ -665,16 +710,20 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 r[2] = rb;
                 silu2(x[t], x[t + 1]);
             }
-            const int valid = live ? ntok - 32 * half : 0;
+            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 32 * half : 0;
+            if (valid < 32) {
 #pragma unroll
-            for (int t = 0; t < 32; ++t) {
-                if (t >= valid)
-                    x[t] = 0.f;
-                zero = fmaf(x[t], 0.f, zero);
+                for (int t = 0; t < 32; ++t)
+                    if (t >= valid)
+                        x[t] = 0.f;
             }
+#pragma unroll
+            for (int t = 0; t < 32; ++t)
+                zero = fmaf(x[t], 0.f, zero);
             const int gs = c % K::kGateSlots;
-            if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || !wait_all(kUDone, (c & 1) ^ 1))
-                break;
+            ok = ok && gate_ready(c) && wait_all(kUDone, (c & 1) ^ 1);
+            if (!ok) // keep meeting the other threads of this role
+                continue;
             tc_fence_after();
             const float4 *wt = reinterpret_cast<const float4 *>(gate[gs][hl] + 192 + 32 * half);
 #pragma unroll
@@ -695,8 +744,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             arrive(kGEmpty + gs);
             if (SUMMARY)
                 continue;
-            if (c > 0 && !wait_all(kIDone + ((c - 1) & 1), ((c - 1) >> 1) & 1))
-                break;
+            ok = c == 0 || i_done(c - 1);
+            if (!ok)
+                continue;
             tc_fence_after();
             // A non-finite x would reach the tokens before it in its 16-block (as 0 times it): the
             // product takes 0 instead, and the output is set from that token on.
@@ -709,7 +759,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         x[t] = 0.f;
                     }
             }
-            bad[c & 1][half][row] = first;
+            bad[c & 1][half][row] = (uint8_t)first;
 #pragma unroll
             for (int t = 0; t < 32; t += 16) {
                 uint32_t hi[8], lo[8];
@@ -723,57 +773,52 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             tc_fence_before();
             arrive(kXFull);
         }
-    } else if (wg < 5) { // ---- S: the state, CW columns of a row per thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        const int half = wg - 3;
-        const int tiles = gridDim.x;
+        cp_async_wait();
+    } else if (wg < 7) { // ---- S: the state, CW columns of a row per thread
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int part = wg - 3;
+        const int tiles = gridDim.x, slots = a.segments * a.fine;
+        const int64_t unit0 = ((int64_t)u.n * tiles + u.tile) * slots; // of this sequence and tile in the workspace
         float h[CW];
-        auto seg_at = [&](int s) { // state `s` of this sequence and tile in the workspace
-            return a.seg + ((((int64_t)u.n * tiles + u.tile) * a.segments + s) * 128 + row) * S + CW * half;
-        };
-        auto load_state = [&](const float *src) {
-#pragma unroll
-            for (int i = 0; i < CW; i += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(src + i);
-                h[i] = v.x; h[i + 1] = v.y; h[i + 2] = v.z; h[i + 3] = v.w;
-            }
-        };
+        auto seg_at = [&](int s) { return a.seg + ((unit0 + s) * 128 + row) * S + CW * part; };
         auto store_state = [&](float *dst) {
 #pragma unroll
             for (int i = 0; i < CW; i += 4)
                 *reinterpret_cast<float4 *>(dst + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
         };
-        const int64_t gstate = (((int64_t)u.n * p.H + u.h0) * P + row) * S + CW * half;
+        auto add_state = [&](const float *src, float d) { // h = d h + src
+#pragma unroll
+            for (int i = 0; i < CW; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + i);
+                h[i] = fmaf(d, h[i], v.x);
+                h[i + 1] = fmaf(d, h[i + 1], v.y);
+                h[i + 2] = fmaf(d, h[i + 2], v.z);
+                h[i + 3] = fmaf(d, h[i + 3], v.w);
+            }
+        };
+        const int64_t gstate = (((int64_t)u.n * p.H + u.h0) * P + row) * S + CW * part;
 #pragma unroll
         for (int i = 0; i < CW; ++i)
             h[i] = 0.f;
-        if (SUMMARY || a.segments == 1) {
+        if (SUMMARY || slots == 1) {
             if (u.seg == 0 && live && p.init_state != nullptr)
-                load_state(p.init_state + gstate);
+                add_state(p.init_state + gstate, 0.f);
             if (SUMMARY && u.seg == 0)
                 store_state(seg_at(0)); // the output pass must not read what it may be asked to overwrite
         } else {
-            // state 1 is the end of segment 0; each later one is its segment's own part
-            load_state(seg_at(u.seg > 0 ? 1 : 0));
-            for (int s = 2; s <= u.seg; ++s) {
-                const float d = a.segdecay[(((int64_t)u.n * tiles + u.tile) * a.segments + s - 1) * 2 + hl];
-                const float *src = seg_at(s);
-#pragma unroll
-                for (int i = 0; i < CW; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src + i);
-                    h[i] = fmaf(d, h[i], v.x);
-                    h[i + 1] = fmaf(d, h[i + 1], v.y);
-                    h[i + 2] = fmaf(d, h[i + 2], v.z);
-                    h[i + 3] = fmaf(d, h[i + 3], v.w);
-                }
-            }
+            // state 1 is the end of the first summary segment; each later one is its segment's own part
+            const int to = u.seg * a.fine;
+            add_state(seg_at(to > 0 ? 1 : 0), 0.f);
+#pragma unroll 1
+            for (int s = 2; s <= to; ++s)
+                add_state(seg_at(s), a.segdecay[(unit0 + s - 1) * 2 + hl]);
         }
         float decay = 1.f;
         bool ok = true;
         for (int c = 0; c <= u.nc; ++c) {
             if (c > 0) {
                 const int gs = (c - 1) % K::kGateSlots;
-                ok = wait_all(kGFull + gs, ((c - 1) / K::kGateSlots) & 1);
+                ok = gate_ready(c - 1);
                 const float gamma = live ? gate[gs][hl][256 + 63] : 0.f;
                 decay *= gamma;
                 arrive(kGEmpty + gs);
@@ -781,15 +826,25 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < CW; i += 16) {
-                    float v[2][8];
-                    tmem_ld8(tmem + lanes + K::kDH + CW * half + i, v[0]);
-                    tmem_ld8(tmem + lanes + K::kDH + CW * half + i + 8, v[1]);
+                if constexpr (CW == 32) {
+                    float v[2][16];
+                    tmem_ld16(tmem + lanes + K::kDH + CW * part, v[0]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        h[i + k] = fmaf(gamma, h[i + k], v[k / 8][k % 8]);
+                        h[k] = fmaf(gamma, h[k], v[0][k]);
+                    tmem_ld16(tmem + lanes + K::kDH + CW * part + 16, v[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        h[16 + k] = fmaf(gamma, h[16 + k], v[1][k]);
+                } else {
+                    float v[16];
+                    tmem_ld16(tmem + lanes + K::kDH + CW * part, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        h[k] = fmaf(gamma, h[k], v[k]);
                 }
             }
             if (c == u.nc)
@@ -801,8 +856,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         split2(h[i + 2 * k], h[i + 2 * k + 1], hi[k], lo[k]);
-                    tmem_st8(tmem + lanes + K::kDH + CW * half + i / 2, hi);
-                    tmem_st8(tmem + lanes + K::kDH + CW * half + CW / 2 + i / 2, lo);
+                    tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
+                    tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
                 }
                 tmem_wait_st();
             }
@@ -811,83 +866,91 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         }
         if (ok && SUMMARY) {
             store_state(seg_at(u.seg + 1));
-            if (lane == 0 && half == 0 && (q & 1) == 0)
-                a.segdecay[(((int64_t)u.n * tiles + u.tile) * a.segments + u.seg) * 2 + hl] = decay;
+            if (lane == 0 && part == 0 && (q & 1) == 0)
+                a.segdecay[(unit0 + u.seg) * 2 + hl] = decay;
         } else if (ok && u.seg == a.segments - 1 && live && p.final_state != nullptr) {
             store_state(p.final_state + gstate);
         }
-    } else { // ---- Y: the output; 32 tokens of a chunk per warpgroup
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        const int half = wg - 5;
-        const int64_t ys = (int64_t)p.H * P;
+    } else { // ---- Y: the output
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        const int64_t ys = (int64_t)p.H * P, tok0 = u.start + u.c0 * kQ;
+        const uint32_t zbuf = base + K::kOffZ;
+        const int me = tid - 7 * 128;
+        bool ok = true;
+        const T *zr = reinterpret_cast<const T *>(sm + K::kOffZ) + row;
+        if (!SUMMARY && p.z != nullptr && u.nc > 0)
+            copy_rows(zbuf, p.z, p.z_stride, tok0, 1, 0, me, 128);
         for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
-            const int64_t t0 = u.start + (u.c0 + c) * kQ;
-            const int ntok = (int)(u.end - t0 < kQ ? u.end - t0 : kQ), last = ntok - 1;
+            const int64_t t0 = tok0 + c * kQ;
+            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) : 0;
             const int gs = c % K::kGateSlots;
-            const T *zc = reinterpret_cast<const T *>(p.z) + t0 * p.z_stride + (live ? chan : chan - 64);
-            if (p.z != nullptr) { // the next chunk's gate inputs to L2, a 128-byte line per thread
-                const int t = kQ + (tid & 63), line = (tid >> 6) & 3;
-                if (t0 + t < u.end && line < (int)sizeof(T))
-                    prefetch_l2(zc - row + line * (128 / sizeof(T)) + t * p.z_stride);
-            }
-            T raw[8]; // z of 8 tokens, on its way while what comes before it is worked on
-            auto load_z = [&](int first) {
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    raw[t] = zc[(int64_t)(first + t < last ? first + t : last) * p.z_stride];
-            };
-            if (p.z != nullptr)
-                load_z(32 * half);
-            if (!wait_all(kGFull + gs, (c / K::kGateSlots) & 1) || !wait_all(kIDone + (c & 1), (c >> 1) & 1))
-                break;
-            tc_fence_after();
-            int nf = bad[c & 1][0][row];
-            if (half == 1)
-                nf = min(nf, bad[c & 1][1][row]);
-#pragma unroll 1
-            for (int first = 32 * half; first < 32 * half + 32; first += 8) {
-                float y[8], e[8];
-                tmem_ld8(tmem + lanes + K::kYI + first, y);
-                tmem_ld8(tmem + lanes + K::kYA + 64 * hl + first, e);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 8; k += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(gate[gs][hl] + 256 + first + k);
-                    y[k] = fmaf(f.x, y[k], e[k]);
-                    y[k + 1] = fmaf(f.y, y[k + 1], e[k + 1]);
-                    y[k + 2] = fmaf(f.z, y[k + 2], e[k + 2]);
-                    y[k + 3] = fmaf(f.w, y[k + 3], e[k + 3]);
-                }
-                if (first == 32 * half + 24) {
-                    tc_fence_before();
-                    arrive(kYEmpty);
-                    arrive(kGEmpty + gs);
-                }
+            ok = ok && gate_ready(c) && i_done(c);
+            if (!ok) { // keep meeting the other threads of this role
                 if (p.z != nullptr) {
-#pragma unroll
-                    for (int t = 0; t < 8; t += 2) {
-                        float za = to_f(raw[t]), zb = to_f(raw[t + 1]);
-                        silu2(za, zb);
-                        y[t] *= za;
-                        y[t + 1] *= zb;
-                    }
-                    if (first < 32 * half + 24)
-                        load_z(first + 8);
+                    group_sync(2, 128);
+                    group_sync(2, 128);
                 }
-                if (nf < first + 8) {
+                continue;
+            }
+            tc_fence_after();
+            float y[kQ];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        if (first + t >= nf)
-                            y[t] = __uint_as_float(0x7fffffffu);
+            for (int t = 0; t < kQ; t += 16) {
+                float v[16], e[16];
+                tmem_ld16(tmem + lanes + K::kYI + t, v);
+                tmem_ld16(tmem + lanes + K::kYA + 64 * hl + t, e);
+                tmem_wait_ld();
+                const float4 *eg = reinterpret_cast<const float4 *>(gate[gs][hl] + 256 + t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 f = eg[k];
+                    y[t + 4 * k] = fmaf(f.x, v[4 * k], e[4 * k]);
+                    y[t + 4 * k + 1] = fmaf(f.y, v[4 * k + 1], e[4 * k + 1]);
+                    y[t + 4 * k + 2] = fmaf(f.z, v[4 * k + 2], e[4 * k + 2]);
+                    y[t + 4 * k + 3] = fmaf(f.w, v[4 * k + 3], e[4 * k + 3]);
                 }
-                T *dst = reinterpret_cast<T *>(p.y) + (t0 + first) * ys + chan;
-                const int valid = live ? ntok - first : 0;
+            }
+            const int n0 = bad[c & 1][0][row], n1 = bad[c & 1][1][row];
+            tc_fence_before();
+            arrive(kYEmpty);
+            arrive(kGEmpty + gs);
+            if (min(n0, n1) < kQ) {
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+                for (int t = 0; t < kQ; ++t)
+                    if (t >= min(n0, n1))
+                        y[t] = __uint_as_float(0x7fffffffu);
+            }
+            if (p.z != nullptr) {
+                cp_async_wait();
+                group_sync(2, 128);
+#pragma unroll
+                for (int t = 0; t < kQ; t += 2) {
+                    float za = to_f(zr[t * 128]), zb = to_f(zr[(t + 1) * 128]);
+                    silu2(za, zb);
+                    y[t] *= za;
+                    y[t + 1] *= zb;
+                }
+                group_sync(2, 128); // every thread has read its gates
+                if (c + 1 < u.nc)
+                    copy_rows(zbuf, p.z, p.z_stride, t0 + kQ, 1, 0, me, 128);
+            }
+            T *dst = reinterpret_cast<T *>(p.y) + t0 * ys + chan;
+            if (valid == kQ) {
+#pragma unroll
+                for (int t = 0; t < kQ; ++t) {
+                    *dst = from_f<T>(y[t]);
+                    dst += ys;
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < kQ; ++t) {
                     if (t < valid)
-                        dst[t * ys] = from_f<T>(y[t]);
+                        *dst = from_f<T>(y[t]);
+                    dst += ys;
+                }
             }
         }
+        cp_async_wait();
     }
     __syncwarp();
     __syncthreads();
@@ -915,36 +978,44 @@ template <typename T> __global__ void __launch_bounds__(256) ssm_final_conv_kern
         reinterpret_cast<T *>(p.final_conv)[((int64_t)n * 3 + i) * C + c] = v[i];
 }
 
-// The library's choice of segments per sequence, from the time of the busiest
-// SM in chunks: a block's pass over its chunks, and the summary pass before it
-// at about half of that a chunk.
-int choose_segments(int G, int H, int P, int64_t N, int batch) {
-    const int64_t units = (int64_t)batch * G * ((int64_t)(H / G) * P + 127) / 128;
-    const int64_t L = (N / (batch > 0 ? batch : 1) + kQ - 1) / kQ;
-    int best = 1;
-    double cost = 0;
-    for (int s = 1; s <= kMaxSegments && (s == 1 || L / s >= 4); ++s) {
-        const int64_t len = (L + s - 1) / s;
-        const double t = (double)((units * s + kSMs - 1) / kSMs) * len +
-                         (s > 1 ? 3.0 + 0.5 * (double)((units * (s - 1) + kSMs - 1) / kSMs) * len : 0.0);
-        if (s == 1 || t < 0.95 * cost) {
-            best = s;
-            cost = t;
+// The cut of the sequences: segments of the output pass, and how many parts the
+// summary pass before it cuts each into.  Costs are the chunks of the busiest
+// SM; a chunk of the summary pass (no output) is about half of one of the
+// output pass, and the pass itself about three chunks.
+struct Cut {
+    int segments, fine;
+};
+int64_t waves(int64_t blocks) { return (blocks + kSMs - 1) / kSMs; }
+Cut choose_cut(const gdn_ssm_config *c, int64_t N, int batch) {
+    const int64_t units = (int64_t)batch * c->num_groups * (((int64_t)(c->num_heads / c->num_groups) * c->head_dim + 127) / 128);
+    const int64_t L = batch > 0 ? (N / batch + kQ - 1) / kQ : 0;
+    Cut best{1, 1};
+    double cost = (double)(waves(units) * L);
+    const int from = c->segments > 0 ? c->segments : 2, to = c->segments > 0 ? c->segments : kMaxSegments;
+    for (int s = from; s <= to; ++s) {
+        if (c->segments == 0 && L / s < 4)
+            break;
+        for (int f = 1; f <= 4 && s * f <= kMaxSegments && (f == 1 || L / (s * f) >= 4); ++f) {
+            const double t = (double)(waves(units * s) * ((L + s - 1) / s)) +
+                             (s > 1 ? 3.0 + 0.5 * (double)(waves(units * f * (s - 1)) * ((L + s * f - 1) / (s * f))) : 0.0);
+            if ((c->segments > 0 && f == 1) || t < 0.95 * cost) {
+                best = Cut{s, s > 1 ? f : 1};
+                cost = t;
+            }
         }
     }
     return best;
 }
 
 template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaEvent_t begin, cudaEvent_t end, cudaStream_t s) {
-    using K = Scan<P, S>;
-    const int segments = p.N > 0 ? p.segments : 1;
-    const Layout l = layout(p.G, p.H, P, S, p.N, p.batch, segments);
+    using K = Scan<T, P, S>;
+    const Layout l = layout(p.G, p.H, P, S, p.N, p.batch, p.segments * p.fine);
     char *ws = reinterpret_cast<char *>(p.ws);
     uint32_t *status = reinterpret_cast<uint32_t *>(ws);
     const int tpg = (p.H / p.G * P + 127) / 128;
     const int64_t chunks = max_chunks(p.N, p.batch);
     cudaError_t e = cudaSuccess;
-    ScanArgs a{p, (float *)(ws + l.cb), (float *)(ws + l.gates), (float *)(ws + l.seg), (float *)(ws + l.segdecay), status, segments, tpg};
+    ScanArgs a{p, (float *)(ws + l.cb), (float *)(ws + l.gates), (float *)(ws + l.seg), (float *)(ws + l.segdecay), status, p.segments, p.fine, tpg};
     if (p.N > 0) {
         e = cudaFuncSetAttribute(ssm_prep_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem<S>());
         if (e != cudaSuccess)
@@ -954,20 +1025,21 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
         e = record_if(begin, s);
         if (e != cudaSuccess)
             return e;
-        CUtensorMap tbc;
+        CUtensorMap tbc, tcb;
         if (!encode_2d(&tbc, ws + l.bc, 4 * S, (uint64_t)chunks * p.G * kQ, 4 * S * 2, 64, kQ, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
+                       CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
+            !encode_2d(&tcb, ws + l.cb, kQ, (uint64_t)chunks * p.G * kQ, kQ * 4, 32, kQ, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-        if (segments > 1) {
+        if (p.segments > 1) {
             e = cudaFuncSetAttribute(ssm_scan_kernel<T, P, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
             if (e != cudaSuccess)
                 return e;
-            ssm_scan_kernel<T, P, S, true><<<dim3(p.G * tpg, segments - 1, p.batch), kScanThreads, K::kSmem, s>>>(tbc, a);
+            ssm_scan_kernel<T, P, S, true><<<dim3(p.G * tpg, (p.segments - 1) * p.fine, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, a);
         }
         e = cudaFuncSetAttribute(ssm_scan_kernel<T, P, S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
         if (e != cudaSuccess)
             return e;
-        ssm_scan_kernel<T, P, S, false><<<dim3(p.G * tpg, segments, p.batch), kScanThreads, K::kSmem, s>>>(tbc, a);
+        ssm_scan_kernel<T, P, S, false><<<dim3(p.G * tpg, p.segments, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, a);
         e = cudaGetLastError();
         if (e == cudaSuccess)
             e = record_if(end, s);
@@ -991,16 +1063,17 @@ template <typename T> cudaError_t launch_ps(const SsmArgs &p, cudaEvent_t begin,
 
 } // namespace
 
-int ssm_segments(const gdn_ssm_config *c, int batch, int64_t N) {
-    if (N == 0)
-        return 1;
-    return c->segments > 0 ? c->segments : choose_segments(c->num_groups, c->num_heads, c->head_dim, N, batch);
+void ssm_cut(const gdn_ssm_config *c, int batch, int64_t N, int *segments, int *fine) {
+    const Cut k = N > 0 ? choose_cut(c, N, batch) : Cut{1, 1};
+    *segments = k.segments;
+    *fine = k.fine;
 }
 
 size_t ssm_workspace_bytes(const gdn_ssm_config *c, int batch, int64_t N) {
     if (N == 0)
         return 0;
-    return layout(c->num_groups, c->num_heads, c->head_dim, c->state_dim, N, batch, ssm_segments(c, batch, N)).total;
+    const Cut k = choose_cut(c, N, batch);
+    return layout(c->num_groups, c->num_heads, c->head_dim, c->state_dim, N, batch, k.segments * k.fine).total;
 }
 
 // The rows of B and C in the workspace are addressed by 32-bit TMA coordinates.
