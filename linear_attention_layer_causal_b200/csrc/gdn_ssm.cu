@@ -31,7 +31,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kQ = 64;        // tokens of a chunk
-constexpr int kGateRec = 320; // floats of a (chunk, head): G / ln 2, its low part, delta, x' weight, e^G
+constexpr int kGateRec = 320; // floats of a (chunk, head): G / ln 2, its low part, -ln 2 delta, -ln 2 x' weight, e^G
 constexpr int kSMs = 148;
 constexpr uint32_t kStatusTimeout = 1u;
 
@@ -59,36 +59,61 @@ Layout layout(int G, int H, int P, int S, int64_t N, int batch, int slots) {
     return l;
 }
 
-// Two floats as bfloat16 parts: hi = the nearest, lo = what is left, each
-// packed with `a` in the low half.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
-    const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb), "f"(ra));
+// Two floats in one 64-bit register pair: one instruction works on both.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
 }
+__device__ __forceinline__ float2 unpack(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Two floats as bfloat16 parts: hi = the nearest, lo = what is left, each
+// packed with the first in the low half.
+__device__ __forceinline__ void split2(f2 v, uint32_t &hi, uint32_t &lo) {
+    const float2 x = unpack(v);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x.y), "f"(x.x));
+    const f2 h = pack(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+    const float2 l = unpack(fma2(h, pack(-1.f, -1.f), v));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l.y), "f"(l.x));
+}
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) { split2(pack(a, b), hi, lo); }
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float max_nan(float x, float y) {
+__device__ __forceinline__ float rcp(float x) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// SiLU of two values with one reciprocal: 1 / a = b / (a b).  Below -40 the
-// function is taken at -40 (-1.7e-16), so that a b stays below 2^116; the
-// exponents' arguments drop a NaN, so that one value's does not reach the other.
-__device__ __forceinline__ void silu2(float &x, float &y) {
-    const float a = 1.f + ex2(-kLog2e * fmaxf(x, -40.f)), b = 1.f + ex2(-kLog2e * fmaxf(y, -40.f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-    x = max_nan(x, -40.f) * (r * b);
-    y = max_nan(y, -40.f) * (r * a);
-}
+// SiLU(x) = x / (1 + 2^p), p = -x log2(e).
+__device__ __forceinline__ float silu(float x) { return x * rcp(1.f + ex2(-kLog2e * x)); }
+// SiLU(x) / -ln 2 = p / (1 + 2^p).
+__device__ __forceinline__ float silu_scaled(float p) { return p * rcp(1.f + ex2(p)); }
 
 // The row of xbc (or of the window before the sequence) that is token t of
 // sequence n, t >= start - 3; nullptr for a zero row.
@@ -185,8 +210,9 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
             v[1] = fmaf(w[1].w, rd.y, fmaf(w[1].z, rc.y, fmaf(w[1].y, rb.y, fmaf(w[1].x, ra.y, b.y))));
             v[2] = fmaf(w[2].w, rd.z, fmaf(w[2].z, rc.z, fmaf(w[2].y, rb.z, fmaf(w[2].x, ra.z, b.z))));
             v[3] = fmaf(w[3].w, rd.w, fmaf(w[3].z, rc.w, fmaf(w[3].y, rb.w, fmaf(w[3].x, ra.w, b.w))));
-            silu2(v[0], v[1]);
-            silu2(v[2], v[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = silu(v[k]);
             if (r0 + i >= ntok)
                 v[0] = v[1] = v[2] = v[3] = 0.f;
             uint2 h, l;
@@ -239,8 +265,9 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
             const float gh = (float)G2;
             rec[i] = gh;
             rec[64 + i] = (float)(G2 - (double)gh);
-            rec[128 + i] = d[i];
-            rec[192 + i] = d[i] == 0.f ? 0.f : d[i] * expf((float)(all - G));
+            // times -ln 2: the scan kernel's x is SiLU(x) / -ln 2
+            rec[128 + i] = -kLn2 * d[i];
+            rec[192 + i] = d[i] == 0.f ? 0.f : -kLn2 * (d[i] * expf((float)(all - G)));
             rec[256 + i] = expf((float)G);
         }
     }
@@ -460,26 +487,27 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     // Copies of 128 channels (those of absent heads left out) of the tokens first .. kQ - 1 of a chunk to shared
     // memory, by n threads; a token behind the end of the sequence is the last one instead.
     auto copy_rows = [&](uint32_t dst, const void *src, int64_t stride, int64_t t0, int c, int first, int me, int n) {
-        constexpr int PIECES = K::kRow / 16;
-        const int last = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 1;
-        const int pieces = u.nh * (P * (int)sizeof(T) / 16);
-        for (int i = me; i < (kQ - first) * PIECES; i += n) {
-            const int t = first + i / PIECES, k = i % PIECES;
-            const T *at = reinterpret_cast<const T *>(src) + (t0 + (t < last ? t : last)) * stride;
-            bool zeros = false;
-            if (t < 0 && c == 0) { // before the segment: the window, or the rows of the segment ahead
-                const T *row_before = conv_row<T>(p, u.n, u.start, t0 + t);
-                zeros = row_before == nullptr;
-                at = zeros ? reinterpret_cast<const T *>(src) : row_before;
-            }
-            if (k < pieces)
-                cp_async16(dst + (t - first) * K::kRow + 16 * k, at + u.h0 * P + k * (16 / (int)sizeof(T)), zeros);
+        constexpr int PIECES = K::kRow / 16; // a thread keeps its piece of the rows
+        const int last = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 1, k = me % PIECES, step = n / PIECES;
+        if (k >= u.nh * (P * (int)sizeof(T) / 16))
+            return;
+        const int col = u.h0 * P + k * (16 / (int)sizeof(T));
+        const T *from = reinterpret_cast<const T *>(src) + t0 * stride + col;
+        uint32_t to = dst + (me / PIECES) * K::kRow + 16 * k;
+        int t = first + me / PIECES;
+        if (t < 0 && c == 0) { // before the segment: the window, or the rows of the segment ahead
+            const T *row_before = conv_row<T>(p, u.n, u.start, t0 + t);
+            cp_async16(to, row_before == nullptr ? from : row_before + col, row_before == nullptr);
+            t += step;
+            to += step * K::kRow;
         }
+        for (; t < kQ; t += step, to += step * K::kRow)
+            cp_async16(to, from + (t < last ? t : last) * stride, false);
     };
 
     if (wg == 0) {
-        // 128 x (56 + 2 x 64 + 4 x 56 + 96) registers, of 1024 x 64 that the block was launched with
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // 128 x (72 + 2 x 64 + 4 x 56 + 80) registers, of 1024 x 64 that the block was launched with
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 72;");
         if (warp == 0) {
             if (lane == 0) { // ---- loads
                 const int gbytes = u.nh * kGateRec * 4;
@@ -608,8 +636,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             }
         } else { // ---- M: the decay masks times C B^T, as operands; two warps
             const int odd = lane & 1; // a thread has a row and every other group of 8 columns
-            const float D0 = p.D != nullptr ? __ldg(p.D + u.h0) : 0.f;
-            const float D1 = p.D != nullptr && u.nh > 1 ? __ldg(p.D + u.h0 + 1) : 0.f;
+            const float D0 = p.D != nullptr ? -kLn2 * __ldg(p.D + u.h0) : 0.f;
+            const float D1 = p.D != nullptr && u.nh > 1 ? -kLn2 * __ldg(p.D + u.h0 + 1) : 0.f;
             for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
                 const int mb = c % K::kMBufs, gs = c % K::kGateSlots;
                 // the chunk that last had this buffer: its products are done
@@ -626,35 +654,36 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     // two boxes of 32 columns, 16-byte pieces swizzled by the row
                     const uint8_t *cbr = sm + K::kOffCb + (s0 >> 5) * 8192 + t * 128;
                     const int piece = (s0 & 31) >> 2;
-                    float v[8];
-                    *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(cbr + ((piece ^ (t & 7)) << 4));
-                    *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(cbr + (((piece + 1) ^ (t & 7)) << 4));
-#pragma unroll 1
-                    for (int h = 0; h < u.nh; ++h) {
+                    f2 v[4];
+                    *reinterpret_cast<ulonglong2 *>(v) = *reinterpret_cast<const ulonglong2 *>(cbr + ((piece ^ (t & 7)) << 4));
+                    *reinterpret_cast<ulonglong2 *>(v + 2) = *reinterpret_cast<const ulonglong2 *>(cbr + (((piece + 1) ^ (t & 7)) << 4));
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) { // an absent head's mask is never used
                         const float *rec = gate[gs][h];
-                        const float gh = rec[t], gl = rec[64 + t];
+                        const f2 gh = pack(rec[t], rec[t]), gl = pack(rec[64 + t], rec[64 + t]), minus = pack(-1.f, -1.f);
                         uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            const float4 sh = *reinterpret_cast<const float4 *>(rec + s0 + k);
-                            const float4 sl = *reinterpret_cast<const float4 *>(rec + 64 + s0 + k);
-                            const float4 sd = *reinterpret_cast<const float4 *>(rec + 128 + s0 + k);
-                            float m[4];
-                            m[0] = ex2((gh - sh.x) + (gl - sl.x)) * (sd.x * v[k]);
-                            m[1] = ex2((gh - sh.y) + (gl - sl.y)) * (sd.y * v[k + 1]);
-                            m[2] = ex2((gh - sh.z) + (gl - sl.z)) * (sd.z * v[k + 2]);
-                            m[3] = ex2((gh - sh.w) + (gl - sl.w)) * (sd.w * v[k + 3]);
+                        for (int k = 0; k < 4; k += 2) {
+                            const ulonglong2 sh = *reinterpret_cast<const ulonglong2 *>(rec + s0 + 2 * k);
+                            const ulonglong2 sl = *reinterpret_cast<const ulonglong2 *>(rec + 64 + s0 + 2 * k);
+                            const ulonglong2 sd = *reinterpret_cast<const ulonglong2 *>(rec + 128 + s0 + 2 * k);
+                            float2 d0 = unpack(add2(fma2(sh.x, minus, gh), fma2(sl.x, minus, gl)));
+                            float2 d1 = unpack(add2(fma2(sh.y, minus, gh), fma2(sl.y, minus, gl)));
+                            f2 m0 = mul2(pack(ex2(d0.x), ex2(d0.y)), mul2(sd.x, v[k]));
+                            f2 m1 = mul2(pack(ex2(d1.x), ex2(d1.y)), mul2(sd.y, v[k + 1]));
                             if (i == rb) { // the diagonal block
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    if (s0 + k + j > t)
-                                        m[j] = 0.f;
-                                    if (s0 + k + j == t)
-                                        m[j] += h == 0 ? D0 : D1;
-                                }
+                                const float Dh = h == 0 ? D0 : D1;
+                                float2 a0 = unpack(m0), a1 = unpack(m1);
+                                const int at = t - s0 - 2 * k; // the diagonal's column among the four
+                                a0.x = at < 0 ? 0.f : at == 0 ? a0.x + Dh : a0.x;
+                                a0.y = at < 1 ? 0.f : at == 1 ? a0.y + Dh : a0.y;
+                                a1.x = at < 2 ? 0.f : at == 2 ? a1.x + Dh : a1.x;
+                                a1.y = at < 3 ? 0.f : at == 3 ? a1.y + Dh : a1.y;
+                                m0 = pack(a0.x, a0.y);
+                                m1 = pack(a1.x, a1.y);
                             }
-                            split2(m[0], m[1], hi[k / 2], lo[k / 2]);
-                            split2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
+                            split2(m0, hi[k], lo[k]);
+                            split2(m1, hi[k + 1], lo[k + 1]);
                         }
                         // K-major rows of 128 bytes, 16-byte pieces swizzled by the row
                         const uint32_t at = mbuf + h * 2 * kQ * kQ * 2 + t * 128 + (((s0 >> 3) ^ (t & 7)) << 4);
@@ -672,11 +701,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         const int half = wg - 1, me = tid - 128;
         const uint32_t xbuf = base + K::kOffX;
         float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f;
-        if (live) {
+        if (live) { // times -log2(e), as the exponential of the SiLU takes its argument
             const float4 w = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + chan);
-            w0 = w.x; w1 = w.y; w2 = w.z; w3 = w.w;
+            w0 = -kLog2e * w.x; w1 = -kLog2e * w.y; w2 = -kLog2e * w.z; w3 = -kLog2e * w.w;
             if (p.conv_b != nullptr)
-                wb = __ldg(p.conv_b + chan);
+                wb = -kLog2e * __ldg(p.conv_b + chan);
         }
         const int64_t tok0 = u.start + u.c0 * kQ;
         bool ok = true;
@@ -686,57 +715,54 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             const int64_t t0 = tok0 + c * kQ;
             cp_async_wait();
             group_sync(1, 256); // every thread's copies have landed
-            float x[32], r[3];
+            float r[36]; // tokens -4 (unused), -3, .., 31
+            f2 x[16];
             {
                 const T *src = reinterpret_cast<const T *>(sm + K::kOffX) + (32 * half) * 128 + row;
+                r[0] = 0.f;
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
-                    r[t] = to_f(src[t * 128]);
-#pragma unroll
-                for (int t = 0; t < 32; ++t)
-                    x[t] = to_f(src[(t + 3) * 128]);
+                for (int t = 1; t < 36; ++t)
+                    r[t] = to_f(src[(t - 1) * 128]);
             }
             group_sync(1, 256); // every thread has its tokens
             if (c + 1 < u.nc)
                 copy_rows(xbuf, p.xbc, p.xbc_stride, t0 + kQ, c + 1, -3, me, 256);
-            float zero = 0.f;
+            const f2 p1 = pack(w1, w1), p3 = pack(w3, w3), pb = pack(wb, wb);
 #pragma unroll
-            for (int t = 0; t < 32; t += 2) {
-                const float ra = x[t], rb = x[t + 1];
-                x[t] = fmaf(w3, ra, fmaf(w2, r[2], fmaf(w1, r[1], fmaf(w0, r[0], wb))));
-                x[t + 1] = fmaf(w3, rb, fmaf(w2, ra, fmaf(w1, r[2], fmaf(w0, r[1], wb))));
-                r[0] = r[2];
-                r[1] = ra;
-                r[2] = rb;
-                silu2(x[t], x[t + 1]);
+            for (int t = 0; t < 16; ++t) { // tokens 2 t, 2 t + 1; taps 1 and 3 sit in register pairs
+                const float *v = r + 2 * t;
+                const float2 m = unpack(fma2(p3, pack(v[4], v[5]), fma2(p1, pack(v[2], v[3]), pb)));
+                x[t] = pack(silu_scaled(fmaf(w2, v[3], fmaf(w0, v[1], m.x))), silu_scaled(fmaf(w2, v[4], fmaf(w0, v[2], m.y))));
             }
             const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 32 * half : 0;
             if (valid < 32) {
 #pragma unroll
-                for (int t = 0; t < 32; ++t)
-                    if (t >= valid)
-                        x[t] = 0.f;
+                for (int t = 0; t < 16; ++t) {
+                    const float2 v = unpack(x[t]);
+                    x[t] = pack(2 * t < valid ? v.x : 0.f, 2 * t + 1 < valid ? v.y : 0.f);
+                }
             }
+            f2 zero2 = 0ull;
 #pragma unroll
-            for (int t = 0; t < 32; ++t)
-                zero = fmaf(x[t], 0.f, zero);
+            for (int t = 0; t < 16; ++t)
+                zero2 = fma2(x[t], 0ull, zero2);
             const int gs = c % K::kGateSlots;
             ok = ok && gate_ready(c) && wait_all(kUDone, (c & 1) ^ 1);
             if (!ok) // keep meeting the other threads of this role
                 continue;
             tc_fence_after();
-            const float4 *wt = reinterpret_cast<const float4 *>(gate[gs][hl] + 192 + 32 * half);
+            const ulonglong2 *wt = reinterpret_cast<const ulonglong2 *>(gate[gs][hl] + 192 + 32 * half);
 #pragma unroll
-            for (int t = 0; t < 32; t += 16) {
+            for (int t = 0; t < 16; t += 8) {
                 uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                    const float4 w = wt[(t + k) / 4];
-                    split2(x[t + k] * w.x, x[t + k + 1] * w.y, hi[k / 2], lo[k / 2]);
-                    split2(x[t + k + 2] * w.z, x[t + k + 3] * w.w, hi[k / 2 + 1], lo[k / 2 + 1]);
+                for (int k = 0; k < 8; k += 2) {
+                    const ulonglong2 w = wt[(t + k) / 2];
+                    split2(mul2(x[t + k], w.x), hi[k], lo[k]);
+                    split2(mul2(x[t + k + 1], w.y), hi[k + 1], lo[k + 1]);
                 }
-                tmem_st8(tmem + lanes + K::kXP + 16 * half + t / 2, hi);
-                tmem_st8(tmem + lanes + K::kXP + 32 + 16 * half + t / 2, lo);
+                tmem_st8(tmem + lanes + K::kXP + 16 * half + t, hi);
+                tmem_st8(tmem + lanes + K::kXP + 32 + 16 * half + t, lo);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -751,23 +777,31 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             // A non-finite x would reach the tokens before it in its 16-block (as 0 times it): the
             // product takes 0 instead, and the output is set from that token on.
             int first = kQ;
-            if (zero != 0.f) {
+            const float2 z = unpack(zero2);
+            if (z.x + z.y != 0.f) {
 #pragma unroll
-                for (int t = 31; t >= 0; --t)
-                    if (!(fabsf(x[t]) <= 3.402823466e38f)) {
-                        first = 32 * half + t;
-                        x[t] = 0.f;
+                for (int t = 15; t >= 0; --t) {
+                    float2 v = unpack(x[t]);
+                    if (!(fabsf(v.y) <= 3.402823466e38f)) {
+                        first = 32 * half + 2 * t + 1;
+                        v.y = 0.f;
                     }
+                    if (!(fabsf(v.x) <= 3.402823466e38f)) {
+                        first = 32 * half + 2 * t;
+                        v.x = 0.f;
+                    }
+                    x[t] = pack(v.x, v.y);
+                }
             }
             bad[c & 1][half][row] = (uint8_t)first;
 #pragma unroll
-            for (int t = 0; t < 32; t += 16) {
+            for (int t = 0; t < 16; t += 8) {
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    split2(x[t + 2 * k], x[t + 2 * k + 1], hi[k], lo[k]);
-                tmem_st8(tmem + lanes + K::kX + 16 * half + t / 2, hi);
-                tmem_st8(tmem + lanes + K::kX + 32 + 16 * half + t / 2, lo);
+                    split2(x[t + k], hi[k], lo[k]);
+                tmem_st8(tmem + lanes + K::kX + 16 * half + t, hi);
+                tmem_st8(tmem + lanes + K::kX + 32 + 16 * half + t, lo);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -779,27 +813,26 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         const int part = wg - 3;
         const int tiles = gridDim.x, slots = a.segments * a.fine;
         const int64_t unit0 = ((int64_t)u.n * tiles + u.tile) * slots; // of this sequence and tile in the workspace
-        float h[CW];
+        f2 h[CW / 2];
         auto seg_at = [&](int s) { return a.seg + ((unit0 + s) * 128 + row) * S + CW * part; };
         auto store_state = [&](float *dst) {
 #pragma unroll
-            for (int i = 0; i < CW; i += 4)
-                *reinterpret_cast<float4 *>(dst + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+            for (int i = 0; i < CW / 2; i += 2)
+                *reinterpret_cast<ulonglong2 *>(dst + 2 * i) = make_ulonglong2(h[i], h[i + 1]);
         };
         auto add_state = [&](const float *src, float d) { // h = d h + src
+            const f2 dd = pack(d, d);
 #pragma unroll
-            for (int i = 0; i < CW; i += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(src + i);
-                h[i] = fmaf(d, h[i], v.x);
-                h[i + 1] = fmaf(d, h[i + 1], v.y);
-                h[i + 2] = fmaf(d, h[i + 2], v.z);
-                h[i + 3] = fmaf(d, h[i + 3], v.w);
+            for (int i = 0; i < CW / 2; i += 2) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(src + 2 * i);
+                h[i] = fma2(dd, h[i], v.x);
+                h[i + 1] = fma2(dd, h[i + 1], v.y);
             }
         };
         const int64_t gstate = (((int64_t)u.n * p.H + u.h0) * P + row) * S + CW * part;
 #pragma unroll
-        for (int i = 0; i < CW; ++i)
-            h[i] = 0.f;
+        for (int i = 0; i < CW / 2; ++i)
+            h[i] = 0ull;
         if (SUMMARY || slots == 1) {
             if (u.seg == 0 && live && p.init_state != nullptr)
                 add_state(p.init_state + gstate, 0.f);
@@ -826,25 +859,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                if constexpr (CW == 32) {
-                    float v[2][16];
-                    tmem_ld16(tmem + lanes + K::kDH + CW * part, v[0]);
-                    tmem_wait_ld();
+                const f2 gg = pack(gamma, gamma);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        h[k] = fmaf(gamma, h[k], v[0][k]);
-                    tmem_ld16(tmem + lanes + K::kDH + CW * part + 16, v[1]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        h[16 + k] = fmaf(gamma, h[16 + k], v[1][k]);
-                } else {
+                for (int i = 0; i < CW; i += 16) {
                     float v[16];
-                    tmem_ld16(tmem + lanes + K::kDH + CW * part, v);
+                    tmem_ld16(tmem + lanes + K::kDH + CW * part + i, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        h[k] = fmaf(gamma, h[k], v[k]);
+                    for (int k = 0; k < 8; ++k)
+                        h[i / 2 + k] = fma2(gg, h[i / 2 + k], pack(v[2 * k], v[2 * k + 1]));
                 }
             }
             if (c == u.nc)
@@ -855,7 +878,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        split2(h[i + 2 * k], h[i + 2 * k + 1], hi[k], lo[k]);
+                        split2(h[i / 2 + k], hi[k], lo[k]);
                     tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
                     tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
                 }
@@ -872,7 +895,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             store_state(p.final_state + gstate);
         }
     } else { // ---- Y: the output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
         const int64_t ys = (int64_t)p.H * P, tok0 = u.start + u.c0 * kQ;
         const uint32_t zbuf = base + K::kOffZ;
         const int me = tid - 7 * 128;
@@ -893,61 +916,65 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 continue;
             }
             tc_fence_after();
-            float y[kQ];
-#pragma unroll
-            for (int t = 0; t < kQ; t += 16) {
-                float v[16], e[16];
-                tmem_ld16(tmem + lanes + K::kYI + t, v);
-                tmem_ld16(tmem + lanes + K::kYA + 64 * hl + t, e);
-                tmem_wait_ld();
-                const float4 *eg = reinterpret_cast<const float4 *>(gate[gs][hl] + 256 + t);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 f = eg[k];
-                    y[t + 4 * k] = fmaf(f.x, v[4 * k], e[4 * k]);
-                    y[t + 4 * k + 1] = fmaf(f.y, v[4 * k + 1], e[4 * k + 1]);
-                    y[t + 4 * k + 2] = fmaf(f.z, v[4 * k + 2], e[4 * k + 2]);
-                    y[t + 4 * k + 3] = fmaf(f.w, v[4 * k + 3], e[4 * k + 3]);
-                }
-            }
-            const int n0 = bad[c & 1][0][row], n1 = bad[c & 1][1][row];
-            tc_fence_before();
-            arrive(kYEmpty);
-            arrive(kGEmpty + gs);
-            if (min(n0, n1) < kQ) {
-#pragma unroll
-                for (int t = 0; t < kQ; ++t)
-                    if (t >= min(n0, n1))
-                        y[t] = __uint_as_float(0x7fffffffu);
-            }
+            const int nf = min(bad[c & 1][0][row], bad[c & 1][1][row]);
+            // 32-bit byte offsets from the chunk's first row: at most 64 H P elements
+            char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + t0 * ys + u.h0 * P);
+            const uint32_t step = (uint32_t)ys * (uint32_t)sizeof(T);
+            uint32_t at = row * (uint32_t)sizeof(T);
             if (p.z != nullptr) {
                 cp_async_wait();
                 group_sync(2, 128);
+            }
+#pragma unroll 1
+            for (int first = 0; first < kQ; first += 32) {
+                f2 y[16];
 #pragma unroll
-                for (int t = 0; t < kQ; t += 2) {
-                    float za = to_f(zr[t * 128]), zb = to_f(zr[(t + 1) * 128]);
-                    silu2(za, zb);
-                    y[t] *= za;
-                    y[t + 1] *= zb;
+                for (int t = 0; t < 32; t += 16) {
+                    float v[16], e[16];
+                    tmem_ld16(tmem + lanes + K::kYI + first + t, v);
+                    tmem_ld16(tmem + lanes + K::kYA + 64 * hl + first + t, e);
+                    tmem_wait_ld();
+                    const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[gs][hl] + 256 + first + t);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const ulonglong2 f = eg[k];
+                        y[t / 2 + 2 * k] = fma2(f.x, pack(v[4 * k], v[4 * k + 1]), pack(e[4 * k], e[4 * k + 1]));
+                        y[t / 2 + 2 * k + 1] = fma2(f.y, pack(v[4 * k + 2], v[4 * k + 3]), pack(e[4 * k + 2], e[4 * k + 3]));
+                    }
                 }
+                if (first == 32) {
+                    tc_fence_before();
+                    arrive(kYEmpty);
+                    arrive(kGEmpty + gs);
+                }
+                if (nf < first + 32) {
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) {
+                        const float2 v = unpack(y[t]);
+                        const float nan = __uint_as_float(0x7fffffffu);
+                        y[t] = pack(first + 2 * t >= nf ? nan : v.x, first + 2 * t + 1 >= nf ? nan : v.y);
+                    }
+                }
+                if (p.z != nullptr) {
+                    const T *z = zr + first * 128;
+#pragma unroll
+                    for (int t = 0; t < 16; ++t)
+                        y[t] = mul2(y[t], pack(silu(to_f(z[2 * t * 128])), silu(to_f(z[(2 * t + 1) * 128]))));
+                }
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    const float2 v = unpack(y[t]);
+                    if (first + 2 * t < valid)
+                        *reinterpret_cast<T *>(dst + at) = from_f<T>(v.x);
+                    if (first + 2 * t + 1 < valid)
+                        *reinterpret_cast<T *>(dst + (at + step)) = from_f<T>(v.y);
+                    at += 2 * step;
+                }
+            }
+            if (p.z != nullptr) {
                 group_sync(2, 128); // every thread has read its gates
                 if (c + 1 < u.nc)
                     copy_rows(zbuf, p.z, p.z_stride, t0 + kQ, 1, 0, me, 128);
-            }
-            T *dst = reinterpret_cast<T *>(p.y) + t0 * ys + chan;
-            if (valid == kQ) {
-#pragma unroll
-                for (int t = 0; t < kQ; ++t) {
-                    *dst = from_f<T>(y[t]);
-                    dst += ys;
-                }
-            } else {
-#pragma unroll
-                for (int t = 0; t < kQ; ++t) {
-                    if (t < valid)
-                        *dst = from_f<T>(y[t]);
-                    dst += ys;
-                }
             }
         }
         cp_async_wait();
