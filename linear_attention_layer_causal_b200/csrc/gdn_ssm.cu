@@ -346,7 +346,7 @@ template <typename T, int P, int S> struct Scan {
     static constexpr int kHalf = 2 * S * kQ * 2;      // bytes of a chunk's B (or C): hi, lo
     static constexpr int kSlots = 3;                  // of them in shared memory: C, B, C, B, ... in turn
     static constexpr int kGateSlots = 4;
-    static constexpr int kMBytes = kHeads * 2 * kQ * kQ * 2; // M hi, lo of each head
+    static constexpr int kMBytes = kHeads * 2 * kQ * kQ * 2; // M hi of the heads, then lo
     static constexpr int kMBufs = sizeof(T) == 2 ? 2 : 1;
     static constexpr int kCbBytes = kQ * kQ * 4;
     static constexpr int kRow = 128 * sizeof(T);      // 128 channels of a token
@@ -360,6 +360,7 @@ template <typename T, int P, int S> struct Scan {
     static constexpr uint32_t kYA = 192;           // x^T M^T, 64 columns per head
     static constexpr uint32_t kXP = 320;           // x' hi, lo
     static constexpr uint32_t kX = 384;            // x hi, lo
+    static constexpr uint32_t kYI2 = 448;          // the other buffer of H C^T
 };
 constexpr int kScanThreads = 1024;
 constexpr uint32_t kTmemCols = 512;
@@ -457,6 +458,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     }
     if (warp == 1)
         tmem_alloc(smem_u32(&tmem_base), kTmemCols);
+    if (!SUMMARY) { // the masks' zeros: what lies above their diagonal blocks is never written
+        for (int i = tid; i < K::kMBufs * K::kMBytes / 16; i += kScanThreads)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + K::kOffM + 16 * i), "r"(0) : "memory");
+        fence_proxy_async_smem();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -573,20 +579,20 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             for (int c = 0; c < u.nc; ++c) {
                 const uint32_t ph = c & 1;
                 if (!SUMMARY) {
-                    ok = wait_all(kBcFull + slot, sph) && wait_all(kHFull, ph) && wait_all(kYEmpty, ph ^ 1);
+                    ok = wait_all(kBcFull + slot, sph) && wait_all(kHFull, ph);
                     if (!ok)
                         break;
                     tc_fence_after();
                     // Y: D[row][t] = sum_s H[row][s] C[t][s].  H hi of 16 columns kk sits beside lo in the
                     // quarter of DH that its S warpgroup owns.
-                    const uint32_t ch = base + slot * K::kHalf, cl = ch + S * 128;
+                    const uint32_t ch = base + slot * K::kHalf, cl = ch + S * 128, yi = tmem + (ph ? K::kYI2 : K::kYI);
 #pragma unroll
                     for (int kk = 0; kk < S / 16; ++kk) {
                         const uint32_t hh = tmem + K::kDH + kk / (CW / 16) * CW + kk % (CW / 16) * 8, hlo = hh + CW / 2;
                         const uint32_t off = kk / 4 * 8192 + kk % 4 * 32;
-                        mma_bf16_ts_if(tmem + K::kYI, hh, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), kk > 0, issue);
-                        mma_bf16_ts_if(tmem + K::kYI, hh, sdesc_sw128(cl + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
-                        mma_bf16_ts_if(tmem + K::kYI, hlo, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
+                        mma_bf16_ts_if(yi, hh, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), kk > 0, issue);
+                        mma_bf16_ts_if(yi, hh, sdesc_sw128(cl + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
+                        mma_bf16_ts_if(yi, hlo, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
                     }
                     mma_commit_if(bar(kBcEmpty + slot), issue);
                     next_slot();
@@ -609,23 +615,20 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 next_slot();
                 if (!SUMMARY) {
                     const int mb = c % K::kMBufs;
-                    ok = wait_all(kXFull, ph) && wait_all(kMFull + mb, (c / K::kMBufs) & 1);
+                    ok = wait_all(kXFull, ph) && wait_all(kMFull + mb, (c / K::kMBufs) & 1) && wait_all(kYEmpty, ph ^ 1);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    // I: D[row][t] = sum_{s <= t} x[row][s] M[t][s] for each head's M; all 128 rows take part, a
-                    // head's rows read their own.  Tokens before a 16-block of s take nothing from it.
-#pragma unroll 1
-                    for (int h = 0; h < u.nh; ++h) {
-                        const uint32_t mh = base + K::kOffM + mb * K::kMBytes + h * 2 * kQ * kQ * 2, ml = mh + kQ * kQ * 2;
+                    // I: D[row][64 h + t] = sum_s x[row][s] M_h[t][s]; a head's rows read their own 64 columns.
+                    // The masks are whole, with zeros above the diagonal: leaving the 16-blocks of zeros out by
+                    // smaller MMAs took 3000 cycles instead of 768 (each then waits for the one before it).
+                    const uint32_t mh = base + K::kOffM + mb * K::kMBytes, ml = mh + NH * kQ * kQ * 2;
 #pragma unroll
-                        for (int kk = 0; kk < kQ / 16; ++kk) {
-                            const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
-                            const uint32_t d = tmem + K::kYA + 64 * h + 16 * kk, off = 2048 * kk + 32 * kk;
-                            mma_bf16_ts_if(d, xh, sdesc_sw128(mh + off, 16, 1024), idesc_bf16(128, 64 - 16 * kk, false), kk > 0, issue);
-                            mma_bf16_ts_if(d, xh, sdesc_sw128(ml + off, 16, 1024), idesc_bf16(128, 64 - 16 * kk, false), 1, issue);
-                            mma_bf16_ts_if(d, xl, sdesc_sw128(mh + off, 16, 1024), idesc_bf16(128, 64 - 16 * kk, false), 1, issue);
-                        }
+                    for (int kk = 0; kk < kQ / 16; ++kk) {
+                        const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
+                        mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), kk > 0, issue);
+                        mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(ml + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
+                        mma_bf16_ts_if(tmem + K::kYA, xl, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
                     }
                     mma_commit_if(bar(kIDone + (c & 1)), issue);
                 }
@@ -686,9 +689,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             split2(m1, hi[k + 1], lo[k + 1]);
                         }
                         // K-major rows of 128 bytes, 16-byte pieces swizzled by the row
-                        const uint32_t at = mbuf + h * 2 * kQ * kQ * 2 + t * 128 + (((s0 >> 3) ^ (t & 7)) << 4);
+                        const uint32_t at = mbuf + h * kQ * kQ * 2 + t * 128 + (((s0 >> 3) ^ (t & 7)) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kQ * kQ * 2), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + NH * kQ * kQ * 2), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
                     }
                 }
                 fence_proxy_async_smem();
@@ -931,7 +934,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
                 for (int t = 0; t < 32; t += 16) {
                     float v[16], e[16];
-                    tmem_ld16(tmem + lanes + K::kYI + first + t, v);
+                    tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + first + t, v);
                     tmem_ld16(tmem + lanes + K::kYA + 64 * hl + first + t, e);
                     tmem_wait_ld();
                     const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[gs][hl] + 256 + first + t);
