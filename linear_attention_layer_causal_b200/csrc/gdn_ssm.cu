@@ -342,7 +342,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 template <typename T, int P, int S> struct Scan {
     static constexpr int kHeads = 128 / P;            // of a block
-    static constexpr int kCW = S / 4;                 // state columns of an S warpgroup
+    static constexpr int kCW = S / 4;                 // state columns of a worker warpgroup
     static constexpr int kHalf = 2 * S * kQ * 2;      // bytes of a chunk's B (or C): hi, lo
     static constexpr int kSlots = 3;                  // of them in shared memory: C, B, C, B, ... in turn
     static constexpr int kGateSlots = 4;
@@ -362,13 +362,13 @@ template <typename T, int P, int S> struct Scan {
     static constexpr uint32_t kX = 384;            // x hi, lo
     static constexpr uint32_t kYI2 = 448;          // the other buffer of H C^T
 };
-constexpr int kScanThreads = 1024;
+constexpr int kScanThreads = 640, kWorkers = 512;
 constexpr uint32_t kTmemCols = 512;
 
 // B and C slots, M buffers, gate slots, and single barriers
 enum Bar {
     kBcFull = 0, kBcEmpty = 3, kMFull = 6, kIDone = 8, kGFull = 10, kGEmpty = 14,
-    kXpFull = 18, kXFull, kHFull, kUDone, kYEmpty, kCbFull, kCbEmpty, kDrain, kBars
+    kHFull = 18, kXFull, kUDone, kCbFull, kCbEmpty, kDrain, kBars
 };
 
 // What a block works on.
@@ -408,8 +408,12 @@ struct ScanArgs {
 __device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Warpgroups: 0 loads, MMAs and M (two warps); 1, 2 X (32 tokens of a chunk
-// each); 3 to 6 S (a quarter of the state's columns each); 7 Y.
+// Warpgroup 0: a warp that loads, a warp that issues the MMAs, two that make M.
+// The other four work in step, each on 16 tokens of a chunk and a quarter of
+// the state's columns: while the tensor core has Y and U of chunk c, they gate
+// and store the output of chunk c - 1 and convolve x of chunk c + 1.  With a
+// role per warpgroup instead (x, state, output) every role was one or two warps
+// of a scheduler, too few to hide their own latencies: 8500 cycles a chunk.
 // SUMMARY: only the states of the segments but the last, from zero (the first
 // from the initial state, which is also copied); no output.
 template <typename T, int P, int S, bool SUMMARY>
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ __align__(16) float gate[K::kGateSlots][NH][kGateRec];
-    __shared__ uint8_t bad[2][2][128]; // per half of a chunk and row: the first token with a non-finite x
+    __shared__ __align__(4) uint8_t bad[2][128][4]; // per row and 16 tokens: the first with a non-finite x, or kQ
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint8_t *sm = smem_raw + (base - smem_u32(smem_raw));
@@ -443,13 +447,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         }
         for (int i = 0; i < K::kGateSlots; ++i) {
             mbar_init(bar(kGFull + i), 1);
-            mbar_init(bar(kGEmpty + i), SUMMARY ? 24 : 30); // X 8, S 16, Y 4 and M 2 warps
+            mbar_init(bar(kGEmpty + i), SUMMARY ? 16 : 18); // the workers' warps, and M's
         }
-        mbar_init(bar(kXpFull), 8);
-        mbar_init(bar(kXFull), 8);
+        mbar_init(bar(kXFull), 16);
         mbar_init(bar(kHFull), 16);
         mbar_init(bar(kUDone), 1);
-        mbar_init(bar(kYEmpty), 4);
         mbar_init(bar(kCbFull), 1);
         mbar_init(bar(kCbEmpty), 2);
         mbar_init(bar(kDrain), 1);
@@ -512,8 +514,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     };
 
     if (wg == 0) {
-        // 128 x (72 + 2 x 64 + 4 x 56 + 80) registers, of 1024 x 64 that the block was launched with
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 72;");
+        // 128 x (64 + 4 x 104) registers are what the block was launched with (640 x 96)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0) {
             if (lane == 0) { // ---- loads
                 const int gbytes = u.nh * kGateRec * 4;
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     mma_commit_if(bar(kBcEmpty + slot), issue);
                     next_slot();
                 }
-                ok = wait_all(kBcFull + slot, sph) && (!SUMMARY || wait_all(kHFull, ph)) && wait_all(kXpFull, ph);
+                ok = wait_all(kBcFull + slot, sph) && (!SUMMARY || wait_all(kHFull, ph));
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 next_slot();
                 if (!SUMMARY) {
                     const int mb = c % K::kMBufs;
-                    ok = wait_all(kXFull, ph) && wait_all(kMFull + mb, (c / K::kMBufs) & 1) && wait_all(kYEmpty, ph ^ 1);
+                    ok = wait_all(kXFull, ph) && wait_all(kMFull + mb, (c / K::kMBufs) & 1);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -700,9 +702,14 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 arrive(kGEmpty + gs);
             }
         }
-    } else if (wg < 3) { // ---- X: convolution of x, then x' and x as operands; 32 tokens of a chunk per warpgroup
-        const int half = wg - 1, me = tid - 128;
-        const uint32_t xbuf = base + K::kOffX;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int part = wg - 1, me = tid - 128;
+        const uint32_t xbuf = base + K::kOffX, zbuf = base + K::kOffZ;
+        const int64_t tok0 = u.start + u.c0 * kQ, ys = (int64_t)p.H * P;
+        const uint32_t ystep = (uint32_t)ys * (uint32_t)sizeof(T);
+        if (u.nc > 0)
+            copy_rows(xbuf, p.xbc, p.xbc_stride, tok0, 0, -3, me, kWorkers);
         float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f;
         if (live) { // times -log2(e), as the exponential of the SiLU takes its argument
             const float4 w = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + chan);
@@ -710,110 +717,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             if (p.conv_b != nullptr)
                 wb = -kLog2e * __ldg(p.conv_b + chan);
         }
-        const int64_t tok0 = u.start + u.c0 * kQ;
-        bool ok = true;
-        if (u.nc > 0)
-            copy_rows(xbuf, p.xbc, p.xbc_stride, tok0, 0, -3, me, 256);
-        for (int c = 0; c < u.nc; ++c) {
-            const int64_t t0 = tok0 + c * kQ;
-            cp_async_wait();
-            group_sync(1, 256); // every thread's copies have landed
-            float r[36]; // tokens -4 (unused), -3, .., 31
-            f2 x[16];
-            {
-                const T *src = reinterpret_cast<const T *>(sm + K::kOffX) + (32 * half) * 128 + row;
-                r[0] = 0.f;
-#pragma unroll
-                for (int t = 1; t < 36; ++t)
-                    r[t] = to_f(src[(t - 1) * 128]);
-            }
-            group_sync(1, 256); // every thread has its tokens
-            if (c + 1 < u.nc)
-                copy_rows(xbuf, p.xbc, p.xbc_stride, t0 + kQ, c + 1, -3, me, 256);
-            const f2 p1 = pack(w1, w1), p3 = pack(w3, w3), pb = pack(wb, wb);
-#pragma unroll
-            for (int t = 0; t < 16; ++t) { // tokens 2 t, 2 t + 1; taps 1 and 3 sit in register pairs
-                const float *v = r + 2 * t;
-                const float2 m = unpack(fma2(p3, pack(v[4], v[5]), fma2(p1, pack(v[2], v[3]), pb)));
-                x[t] = pack(silu_scaled(fmaf(w2, v[3], fmaf(w0, v[1], m.x))), silu_scaled(fmaf(w2, v[4], fmaf(w0, v[2], m.y))));
-            }
-            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 32 * half : 0;
-            if (valid < 32) {
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    const float2 v = unpack(x[t]);
-                    x[t] = pack(2 * t < valid ? v.x : 0.f, 2 * t + 1 < valid ? v.y : 0.f);
-                }
-            }
-            f2 zero2 = 0ull;
-#pragma unroll
-            for (int t = 0; t < 16; ++t)
-                zero2 = fma2(x[t], 0ull, zero2);
-            const int gs = c % K::kGateSlots;
-            ok = ok && gate_ready(c) && wait_all(kUDone, (c & 1) ^ 1);
-            if (!ok) // keep meeting the other threads of this role
-                continue;
-            tc_fence_after();
-            const ulonglong2 *wt = reinterpret_cast<const ulonglong2 *>(gate[gs][hl] + 192 + 32 * half);
-#pragma unroll
-            for (int t = 0; t < 16; t += 8) {
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    const ulonglong2 w = wt[(t + k) / 2];
-                    split2(mul2(x[t + k], w.x), hi[k], lo[k]);
-                    split2(mul2(x[t + k + 1], w.y), hi[k + 1], lo[k + 1]);
-                }
-                tmem_st8(tmem + lanes + K::kXP + 16 * half + t, hi);
-                tmem_st8(tmem + lanes + K::kXP + 32 + 16 * half + t, lo);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(kXpFull);
-            arrive(kGEmpty + gs);
-            if (SUMMARY)
-                continue;
-            ok = c == 0 || i_done(c - 1);
-            if (!ok)
-                continue;
-            tc_fence_after();
-            // A non-finite x would reach the tokens before it in its 16-block (as 0 times it): the
-            // product takes 0 instead, and the output is set from that token on.
-            int first = kQ;
-            const float2 z = unpack(zero2);
-            if (z.x + z.y != 0.f) {
-#pragma unroll
-                for (int t = 15; t >= 0; --t) {
-                    float2 v = unpack(x[t]);
-                    if (!(fabsf(v.y) <= 3.402823466e38f)) {
-                        first = 32 * half + 2 * t + 1;
-                        v.y = 0.f;
-                    }
-                    if (!(fabsf(v.x) <= 3.402823466e38f)) {
-                        first = 32 * half + 2 * t;
-                        v.x = 0.f;
-                    }
-                    x[t] = pack(v.x, v.y);
-                }
-            }
-            bad[c & 1][half][row] = (uint8_t)first;
-#pragma unroll
-            for (int t = 0; t < 16; t += 8) {
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    split2(x[t + k], hi[k], lo[k]);
-                tmem_st8(tmem + lanes + K::kX + 16 * half + t, hi);
-                tmem_st8(tmem + lanes + K::kX + 32 + 16 * half + t, lo);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(kXFull);
-        }
-        cp_async_wait();
-    } else if (wg < 7) { // ---- S: the state, CW columns of a row per thread
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        const int part = wg - 3;
+        // the state: CW columns of a row
         const int tiles = gridDim.x, slots = a.segments * a.fine;
         const int64_t unit0 = ((int64_t)u.n * tiles + u.tile) * slots; // of this sequence and tile in the workspace
         f2 h[CW / 2];
@@ -850,18 +754,52 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 add_state(seg_at(s), a.segdecay[(unit0 + s - 1) * 2 + hl]);
         }
         float decay = 1.f;
-        bool ok = true;
-        for (int c = 0; c <= u.nc; ++c) {
-            if (c > 0) {
-                const int gs = (c - 1) % K::kGateSlots;
-                ok = gate_ready(c - 1);
-                const float gamma = live ? gate[gs][hl][256 + 63] : 0.f;
-                decay *= gamma;
-                arrive(kGEmpty + gs);
-                ok = ok && wait_all(kUDone, (c - 1) & 1);
-                if (!ok)
-                    break;
+        bool ok = true; // when a wait gave up, the rest runs without waiting: every warp still meets the others
+#pragma unroll 1
+        for (int c = -1; c < u.nc; ++c) {
+            const bool more = c + 1 < u.nc;
+            const int64_t t0 = tok0 + (int64_t)c * kQ; // of chunk c
+            // -- x of chunk c + 1: tokens 16 part ..
+            cp_async_wait();
+            group_sync(1, kWorkers); // its rows have landed, and z of chunk c - 1 has been read
+            f2 x[8];
+            if (more) {
+                if (!SUMMARY && c >= 0 && p.z != nullptr)
+                    copy_rows(zbuf, p.z, p.z_stride, t0, 1, 0, me, kWorkers);
+                float r[20]; // tokens -4 (unused), -3, .., 15
+                const T *src = reinterpret_cast<const T *>(sm + K::kOffX) + (16 * part) * 128 + row;
+                r[0] = 0.f;
+#pragma unroll
+                for (int t = 1; t < 20; ++t)
+                    r[t] = to_f(src[(t - 1) * 128]);
+                group_sync(1, kWorkers); // every thread has its tokens
+                if (c + 2 < u.nc)
+                    copy_rows(xbuf, p.xbc, p.xbc_stride, t0 + 2 * kQ, c + 2, -3, me, kWorkers);
+                const f2 p1 = pack(w1, w1), p3 = pack(w3, w3), pb = pack(wb, wb);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) { // tokens 2 t, 2 t + 1; taps 1 and 3 sit in register pairs
+                    const float *v = r + 2 * t;
+                    const float2 m = unpack(fma2(p3, pack(v[4], v[5]), fma2(p1, pack(v[2], v[3]), pb)));
+                    x[t] = pack(silu_scaled(fmaf(w2, v[3], fmaf(w0, v[1], m.x))), silu_scaled(fmaf(w2, v[4], fmaf(w0, v[2], m.y))));
+                }
+                const int valid = live ? (int)(u.end - t0 - kQ < kQ ? u.end - t0 - kQ : kQ) - 16 * part : 0;
+                if (valid < 16) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const float2 v = unpack(x[t]);
+                        x[t] = pack(2 * t < valid ? v.x : 0.f, 2 * t + 1 < valid ? v.y : 0.f);
+                    }
+                }
+            } else {
+                if (!SUMMARY && c >= 0 && p.z != nullptr)
+                    copy_rows(zbuf, p.z, p.z_stride, t0, 1, 0, me, kWorkers);
+            }
+            // -- the state entering chunk c + 1, and x' of that chunk
+            if (c >= 0) {
+                ok = ok && gate_ready(c) && wait_all(kUDone, c & 1);
                 tc_fence_after();
+                const float gamma = live ? gate[c % K::kGateSlots][hl][256 + 63] : 0.f;
+                decay *= gamma;
                 const f2 gg = pack(gamma, gamma);
 #pragma unroll
                 for (int i = 0; i < CW; i += 16) {
@@ -873,23 +811,129 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         h[i / 2 + k] = fma2(gg, h[i / 2 + k], pack(v[2 * k], v[2 * k + 1]));
                 }
             }
-            if (c == u.nc)
-                break;
-            if (!SUMMARY) {
+            if (more) {
+                if (!SUMMARY) {
 #pragma unroll
-                for (int i = 0; i < CW; i += 16) {
-                    uint32_t hi[8], lo[8];
+                    for (int i = 0; i < CW; i += 16) {
+                        uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        split2(h[i / 2 + k], hi[k], lo[k]);
-                    tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
-                    tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
+                        for (int k = 0; k < 8; ++k)
+                            split2(h[i / 2 + k], hi[k], lo[k]);
+                        tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
+                        tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
+                    }
                 }
+                ok = ok && gate_ready(c + 1);
+                const ulonglong2 *wt = reinterpret_cast<const ulonglong2 *>(gate[(c + 1) % K::kGateSlots][hl] + 192 + 16 * part);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    const ulonglong2 w = wt[k / 2];
+                    split2(mul2(x[k], w.x), hi[k], lo[k]);
+                    split2(mul2(x[k + 1], w.y), hi[k + 1], lo[k + 1]);
+                }
+                tmem_st8(tmem + lanes + K::kXP + 8 * part, hi);
+                tmem_st8(tmem + lanes + K::kXP + 32 + 8 * part, lo);
                 tmem_wait_st();
+                tc_fence_before();
+                arrive(kHFull);
             }
-            tc_fence_before();
-            arrive(kHFull);
+            if (SUMMARY) {
+                if (c >= 0)
+                    arrive(kGEmpty + c % K::kGateSlots);
+                continue;
+            }
+            // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
+            f2 y[8];
+            if (c >= 0) {
+                ok = ok && i_done(c);
+                tc_fence_after();
+                float v[16], e[16];
+                tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + 16 * part, v);
+                tmem_ld16(tmem + lanes + K::kYA + 64 * hl + 16 * part, e);
+                tmem_wait_ld();
+                const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[c % K::kGateSlots][hl] + 256 + 16 * part);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const ulonglong2 f = eg[k];
+                    y[2 * k] = fma2(f.x, pack(v[4 * k], v[4 * k + 1]), pack(e[4 * k], e[4 * k + 1]));
+                    y[2 * k + 1] = fma2(f.y, pack(v[4 * k + 2], v[4 * k + 3]), pack(e[4 * k + 2], e[4 * k + 3]));
+                }
+                arrive(kGEmpty + c % K::kGateSlots);
+            }
+            if (more) {
+                // A non-finite x would reach the tokens before it in its chunk (as 0 times it): the
+                // product takes 0 instead, and the output is set from that token on.
+                f2 zero2 = 0ull;
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    zero2 = fma2(x[t], 0ull, zero2);
+                int first = kQ;
+                const float2 z = unpack(zero2);
+                if (z.x + z.y != 0.f) {
+#pragma unroll
+                    for (int t = 7; t >= 0; --t) {
+                        float2 v = unpack(x[t]);
+                        if (!(fabsf(v.y) <= 3.402823466e38f)) {
+                            first = 16 * part + 2 * t + 1;
+                            v.y = 0.f;
+                        }
+                        if (!(fabsf(v.x) <= 3.402823466e38f)) {
+                            first = 16 * part + 2 * t;
+                            v.x = 0.f;
+                        }
+                        x[t] = pack(v.x, v.y);
+                    }
+                }
+                bad[(c + 1) & 1][row][part] = (uint8_t)first;
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    split2(x[k], hi[k], lo[k]);
+                tmem_st8(tmem + lanes + K::kX + 8 * part, hi);
+                tmem_st8(tmem + lanes + K::kX + 32 + 8 * part, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(kXFull);
+            }
+            if (c < 0)
+                continue;
+            // -- the output of chunk c: gate and store
+            const uint32_t nf = *reinterpret_cast<const uint32_t *>(bad[c & 1][row]);
+            if (nf != 0x40404040u) {
+                int first = kQ; // the first bad token up to this part's end
+                for (int k = 0; k <= part; ++k)
+                    first = min(first, (int)bad[c & 1][row][k]);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const float2 v = unpack(y[t]);
+                    const float nan = __uint_as_float(0x7fffffffu);
+                    y[t] = pack(16 * part + 2 * t >= first ? nan : v.x, 16 * part + 2 * t + 1 >= first ? nan : v.y);
+                }
+            }
+            if (p.z != nullptr) {
+                cp_async_wait();
+                group_sync(1, kWorkers); // z of this chunk has landed
+                const T *zr = reinterpret_cast<const T *>(sm + K::kOffZ) + (16 * part) * 128 + row;
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    y[t] = mul2(y[t], pack(silu(to_f(zr[2 * t * 128])), silu(to_f(zr[(2 * t + 1) * 128]))));
+            }
+            // 32-bit byte offsets from the chunk's first row: at most 64 H P elements
+            char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + t0 * ys + u.h0 * P);
+            uint32_t at = row * (uint32_t)sizeof(T) + 16 * part * ystep;
+            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part : 0;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 v = unpack(y[t]);
+                if (2 * t < valid)
+                    *reinterpret_cast<T *>(dst + at) = from_f<T>(v.x);
+                if (2 * t + 1 < valid)
+                    *reinterpret_cast<T *>(dst + (at + ystep)) = from_f<T>(v.y);
+                at += 2 * ystep;
+            }
         }
+        cp_async_wait();
         if (ok && SUMMARY) {
             store_state(seg_at(u.seg + 1));
             if (lane == 0 && part == 0 && (q & 1) == 0)
@@ -897,90 +941,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         } else if (ok && u.seg == a.segments - 1 && live && p.final_state != nullptr) {
             store_state(p.final_state + gstate);
         }
-    } else { // ---- Y: the output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
-        const int64_t ys = (int64_t)p.H * P, tok0 = u.start + u.c0 * kQ;
-        const uint32_t zbuf = base + K::kOffZ;
-        const int me = tid - 7 * 128;
-        bool ok = true;
-        const T *zr = reinterpret_cast<const T *>(sm + K::kOffZ) + row;
-        if (!SUMMARY && p.z != nullptr && u.nc > 0)
-            copy_rows(zbuf, p.z, p.z_stride, tok0, 1, 0, me, 128);
-        for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
-            const int64_t t0 = tok0 + c * kQ;
-            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) : 0;
-            const int gs = c % K::kGateSlots;
-            ok = ok && gate_ready(c) && i_done(c);
-            if (!ok) { // keep meeting the other threads of this role
-                if (p.z != nullptr) {
-                    group_sync(2, 128);
-                    group_sync(2, 128);
-                }
-                continue;
-            }
-            tc_fence_after();
-            const int nf = min(bad[c & 1][0][row], bad[c & 1][1][row]);
-            // 32-bit byte offsets from the chunk's first row: at most 64 H P elements
-            char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + t0 * ys + u.h0 * P);
-            const uint32_t step = (uint32_t)ys * (uint32_t)sizeof(T);
-            uint32_t at = row * (uint32_t)sizeof(T);
-            if (p.z != nullptr) {
-                cp_async_wait();
-                group_sync(2, 128);
-            }
-#pragma unroll 1
-            for (int first = 0; first < kQ; first += 32) {
-                f2 y[16];
-#pragma unroll
-                for (int t = 0; t < 32; t += 16) {
-                    float v[16], e[16];
-                    tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + first + t, v);
-                    tmem_ld16(tmem + lanes + K::kYA + 64 * hl + first + t, e);
-                    tmem_wait_ld();
-                    const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[gs][hl] + 256 + first + t);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const ulonglong2 f = eg[k];
-                        y[t / 2 + 2 * k] = fma2(f.x, pack(v[4 * k], v[4 * k + 1]), pack(e[4 * k], e[4 * k + 1]));
-                        y[t / 2 + 2 * k + 1] = fma2(f.y, pack(v[4 * k + 2], v[4 * k + 3]), pack(e[4 * k + 2], e[4 * k + 3]));
-                    }
-                }
-                if (first == 32) {
-                    tc_fence_before();
-                    arrive(kYEmpty);
-                    arrive(kGEmpty + gs);
-                }
-                if (nf < first + 32) {
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float2 v = unpack(y[t]);
-                        const float nan = __uint_as_float(0x7fffffffu);
-                        y[t] = pack(first + 2 * t >= nf ? nan : v.x, first + 2 * t + 1 >= nf ? nan : v.y);
-                    }
-                }
-                if (p.z != nullptr) {
-                    const T *z = zr + first * 128;
-#pragma unroll
-                    for (int t = 0; t < 16; ++t)
-                        y[t] = mul2(y[t], pack(silu(to_f(z[2 * t * 128])), silu(to_f(z[(2 * t + 1) * 128]))));
-                }
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    const float2 v = unpack(y[t]);
-                    if (first + 2 * t < valid)
-                        *reinterpret_cast<T *>(dst + at) = from_f<T>(v.x);
-                    if (first + 2 * t + 1 < valid)
-                        *reinterpret_cast<T *>(dst + (at + step)) = from_f<T>(v.y);
-                    at += 2 * step;
-                }
-            }
-            if (p.z != nullptr) {
-                group_sync(2, 128); // every thread has read its gates
-                if (c + 1 < u.nc)
-                    copy_rows(zbuf, p.z, p.z_stride, t0 + kQ, 1, 0, me, 128);
-            }
-        }
-        cp_async_wait();
     }
     __syncwarp();
     __syncthreads();
