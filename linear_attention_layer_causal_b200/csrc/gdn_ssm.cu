@@ -59,7 +59,8 @@ Layout layout(int G, int H, int P, int S, int64_t N, int batch, int slots) {
     return l;
 }
 
-// Two floats in one 64-bit register pair: one instruction works on both.
+// Two floats in one 64-bit register pair, for values that sit in such pairs anyway
+// (elsewhere the moves cost more than the paired instruction saves).
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pack(float x, float y) {
     f2 r;
@@ -76,27 +77,25 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Two floats as bfloat16 parts: hi = the nearest, lo = what is left, each
 // packed with the first in the low half.
-__device__ __forceinline__ void split2(f2 v, uint32_t &hi, uint32_t &lo) {
-    const float2 x = unpack(v);
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x.y), "f"(x.x));
-    const f2 h = pack(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
-    const float2 l = unpack(fma2(h, pack(-1.f, -1.f), v));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l.y), "f"(l.x));
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb), "f"(ra));
 }
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) { split2(pack(a, b), hi, lo); }
+
+// Two outputs to their rows in shared memory, one conversion for both.
+__device__ __forceinline__ void put2(__nv_bfloat16 *p, __nv_bfloat16 *q, float a, float b) {
+    uint32_t v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(b), "f"(a));
+    *reinterpret_cast<uint16_t *>(p) = (uint16_t)v;
+    *reinterpret_cast<uint16_t *>(q) = (uint16_t)(v >> 16);
+}
+__device__ __forceinline__ void put2(float *p, float *q, float a, float b) {
+    *p = a;
+    *q = b;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -143,7 +142,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One chunk and group.  Writes, for the scan kernel: the rows [64][4 S] of
+// One chunk and group; the blocks of z = 1 have the gates.  Writes, for the scan kernel: the rows [64][4 S] of
 // B hi | B lo | C hi | C lo (zero behind the sequence's end), the 64 x 64
 // products C_t . B_s of s's and t's 16-blocks with s <= t, and a gate record
 // for each head of the group.
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
     constexpr int LDS = S + 8; // row length in shared memory: rows 16 bytes apart in banks
     const int64_t id = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (id == 0 && g == 0 && tid == 0)
+    if (id == 0 && g == 0 && blockIdx.z == 0 && tid == 0)
         *status = 0;
     // the sequence of this chunk number: the last n with first_chunk(cu[n]) <= id
     int lo = 0, hi = p.batch - 1;
@@ -175,6 +174,55 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
         return; // a number without a chunk
     const int ntok = (int)(end - t0 < kQ ? end - t0 : kQ);
     const int C = p.conv_dim();
+
+    if (blockIdx.z == 1) { // gates: a warp per head, two neighbouring tokens per lane
+        const int hpg = p.H / p.G;
+        for (int k = warp; k < hpg; k += kPrepThreads / 32) {
+            const int h = g * hpg + k;
+            const double A = -(double)expf(__ldg(p.A_log + h));
+            const float bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.f;
+            float d[2];
+            double s[2];
+    #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                d[i] = 0.f;
+                s[i] = 0.0;
+                if (t < ntok) {
+                    d[i] = ssm_delta(to_f(reinterpret_cast<const T *>(p.dt)[(t0 + t) * p.dt_stride + h]), bias, p.dt_min, p.dt_max);
+                    // no decay below e^-10000 (zero in float32) and no increase; a NaN stays
+                    const double a = d[i] == 0.f ? 0.0 : A * (double)d[i];
+                    s[i] = a < -1e4 ? -1e4 : a;
+                }
+            }
+            s[1] += s[0];
+            double sum = s[1];
+    #pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o)
+                    sum += up;
+            }
+            double before = __shfl_up_sync(0xffffffffu, sum, 1);
+            if (lane == 0)
+                before = 0.0;
+            const double all = __shfl_sync(0xffffffffu, sum, 31);
+            float *rec = gates + (id * p.H + h) * kGateRec + 2 * lane;
+    #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const double G = before + s[i];
+                const double G2 = G * 1.4426950408889634; // for base-2 exponentials
+                const float gh = (float)G2;
+                rec[i] = gh;
+                rec[64 + i] = (float)(G2 - (double)gh);
+                // times -ln 2: the scan kernel's x is SiLU(x) / -ln 2
+                rec[128 + i] = -kLn2 * d[i];
+                rec[192 + i] = d[i] == 0.f ? 0.f : -kLn2 * (d[i] * expf((float)(all - G)));
+                rec[256 + i] = expf((float)G);
+            }
+        }
+        return;
+    }
 
     // convolution and SiLU of four channels for a run of tokens
     constexpr int QUADS = 2 * S / 4, RUNS = kPrepThreads / QUADS, RUN = kQ / RUNS;
@@ -225,52 +273,6 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
         }
     }
 
-    // gates: a warp per head, two neighbouring tokens per lane
-    const int hpg = p.H / p.G;
-    for (int k = warp; k < hpg; k += kPrepThreads / 32) {
-        const int h = g * hpg + k;
-        const double A = -(double)expf(__ldg(p.A_log + h));
-        const float bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.f;
-        float d[2];
-        double s[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * lane + i;
-            d[i] = 0.f;
-            s[i] = 0.0;
-            if (t < ntok) {
-                d[i] = ssm_delta(to_f(reinterpret_cast<const T *>(p.dt)[(t0 + t) * p.dt_stride + h]), bias, p.dt_min, p.dt_max);
-                // no decay below e^-10000 (zero in float32) and no increase; a NaN stays
-                const double a = d[i] == 0.f ? 0.0 : A * (double)d[i];
-                s[i] = a < -1e4 ? -1e4 : a;
-            }
-        }
-        s[1] += s[0];
-        double sum = s[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o)
-                sum += up;
-        }
-        double before = __shfl_up_sync(0xffffffffu, sum, 1);
-        if (lane == 0)
-            before = 0.0;
-        const double all = __shfl_sync(0xffffffffu, sum, 31);
-        float *rec = gates + (id * p.H + h) * kGateRec + 2 * lane;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const double G = before + s[i];
-            const double G2 = G * 1.4426950408889634; // for base-2 exponentials
-            const float gh = (float)G2;
-            rec[i] = gh;
-            rec[64 + i] = (float)(G2 - (double)gh);
-            // times -ln 2: the scan kernel's x is SiLU(x) / -ln 2
-            rec[128 + i] = -kLn2 * d[i];
-            rec[192 + i] = d[i] == 0.f ? 0.f : -kLn2 * (d[i] * expf((float)(all - G)));
-            rec[256 + i] = expf((float)G);
-        }
-    }
     __syncthreads();
 
     // C B^T: warp w has rows 16 (w % 4) .., columns 32 (w / 4) ..
@@ -473,7 +475,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     // A wait that runs out (about a second) makes every role stop at its next
     // wait; what is in flight is waited for before the block ends.
     auto wait = [&](int i, uint32_t parity) {
-        const bool ok = !*abort_v && mbar_wait_sleeping(bar(i), parity, kDefaultWaitLimit);
+        bool ok = mbar_test_wait(bar(i), parity);
+        if (!ok)
+            ok = !*abort_v && mbar_wait_sleeping(bar(i), parity, kDefaultWaitLimit);
         if (!ok) {
             *abort_v = 1;
             atomicOr(a.status, kStatusTimeout);
@@ -492,27 +496,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const int hl = P == 64 ? q >> 1 : 0;    // its head within the block (uniform over the warp)
     const bool live = hl < u.nh;
     const int64_t chan = (int64_t)u.h0 * P + row; // its x channel
-    // Copies of 128 channels (those of absent heads left out) of the tokens first .. kQ - 1 of a chunk to shared
-    // memory, by n threads; a token behind the end of the sequence is the last one instead.
-    auto copy_rows = [&](uint32_t dst, const void *src, int64_t stride, int64_t t0, int c, int first, int me, int n) {
-        constexpr int PIECES = K::kRow / 16; // a thread keeps its piece of the rows
-        const int last = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 1, k = me % PIECES, step = n / PIECES;
-        if (k >= u.nh * (P * (int)sizeof(T) / 16))
-            return;
-        const int col = u.h0 * P + k * (16 / (int)sizeof(T));
-        const T *from = reinterpret_cast<const T *>(src) + t0 * stride + col;
-        uint32_t to = dst + (me / PIECES) * K::kRow + 16 * k;
-        int t = first + me / PIECES;
-        if (t < 0 && c == 0) { // before the segment: the window, or the rows of the segment ahead
-            const T *row_before = conv_row<T>(p, u.n, u.start, t0 + t);
-            cp_async16(to, row_before == nullptr ? from : row_before + col, row_before == nullptr);
-            t += step;
-            to += step * K::kRow;
-        }
-        for (; t < kQ; t += step, to += step * K::kRow)
-            cp_async16(to, from + (t < last ? t : last) * stride, false);
-    };
-
     if (wg == 0) {
         // 128 x (64 + 4 x 104) registers are what the block was launched with (640 x 96)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -659,36 +642,32 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     // two boxes of 32 columns, 16-byte pieces swizzled by the row
                     const uint8_t *cbr = sm + K::kOffCb + (s0 >> 5) * 8192 + t * 128;
                     const int piece = (s0 & 31) >> 2;
-                    f2 v[4];
-                    *reinterpret_cast<ulonglong2 *>(v) = *reinterpret_cast<const ulonglong2 *>(cbr + ((piece ^ (t & 7)) << 4));
-                    *reinterpret_cast<ulonglong2 *>(v + 2) = *reinterpret_cast<const ulonglong2 *>(cbr + (((piece + 1) ^ (t & 7)) << 4));
+                    float v[8];
+                    *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(cbr + ((piece ^ (t & 7)) << 4));
+                    *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(cbr + (((piece + 1) ^ (t & 7)) << 4));
 #pragma unroll
                     for (int h = 0; h < NH; ++h) { // an absent head's mask is never used
                         const float *rec = gate[gs][h];
-                        const f2 gh = pack(rec[t], rec[t]), gl = pack(rec[64 + t], rec[64 + t]), minus = pack(-1.f, -1.f);
+                        const float gh = rec[t], gl = rec[64 + t], Dh = h == 0 ? D0 : D1;
                         uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int k = 0; k < 4; k += 2) {
-                            const ulonglong2 sh = *reinterpret_cast<const ulonglong2 *>(rec + s0 + 2 * k);
-                            const ulonglong2 sl = *reinterpret_cast<const ulonglong2 *>(rec + 64 + s0 + 2 * k);
-                            const ulonglong2 sd = *reinterpret_cast<const ulonglong2 *>(rec + 128 + s0 + 2 * k);
-                            float2 d0 = unpack(add2(fma2(sh.x, minus, gh), fma2(sl.x, minus, gl)));
-                            float2 d1 = unpack(add2(fma2(sh.y, minus, gh), fma2(sl.y, minus, gl)));
-                            f2 m0 = mul2(pack(ex2(d0.x), ex2(d0.y)), mul2(sd.x, v[k]));
-                            f2 m1 = mul2(pack(ex2(d1.x), ex2(d1.y)), mul2(sd.y, v[k + 1]));
+                        for (int k = 0; k < 8; k += 4) {
+                            const float4 sh = *reinterpret_cast<const float4 *>(rec + s0 + k);
+                            const float4 sl = *reinterpret_cast<const float4 *>(rec + 64 + s0 + k);
+                            const float4 sd = *reinterpret_cast<const float4 *>(rec + 128 + s0 + k);
+                            float m[4];
+                            m[0] = ex2((gh - sh.x) + (gl - sl.x)) * (sd.x * v[k]);
+                            m[1] = ex2((gh - sh.y) + (gl - sl.y)) * (sd.y * v[k + 1]);
+                            m[2] = ex2((gh - sh.z) + (gl - sl.z)) * (sd.z * v[k + 2]);
+                            m[3] = ex2((gh - sh.w) + (gl - sl.w)) * (sd.w * v[k + 3]);
                             if (i == rb) { // the diagonal block
-                                const float Dh = h == 0 ? D0 : D1;
-                                float2 a0 = unpack(m0), a1 = unpack(m1);
-                                const int at = t - s0 - 2 * k; // the diagonal's column among the four
-                                a0.x = at < 0 ? 0.f : at == 0 ? a0.x + Dh : a0.x;
-                                a0.y = at < 1 ? 0.f : at == 1 ? a0.y + Dh : a0.y;
-                                a1.x = at < 2 ? 0.f : at == 2 ? a1.x + Dh : a1.x;
-                                a1.y = at < 3 ? 0.f : at == 3 ? a1.y + Dh : a1.y;
-                                m0 = pack(a0.x, a0.y);
-                                m1 = pack(a1.x, a1.y);
+                                const int at = t - s0 - k; // the diagonal's column among the four
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    m[j] = at < j ? 0.f : at == j ? m[j] + Dh : m[j];
                             }
-                            split2(m0, hi[k], lo[k]);
-                            split2(m1, hi[k + 1], lo[k + 1]);
+                            split2(m[0], m[1], hi[k / 2], lo[k / 2]);
+                            split2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
                         }
                         // K-major rows of 128 bytes, 16-byte pieces swizzled by the row
                         const uint32_t at = mbuf + h * kQ * kQ * 2 + t * 128 + (((s0 >> 3) ^ (t & 7)) << 4);
@@ -707,9 +686,40 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         const int part = wg - 1, me = tid - 128;
         const uint32_t xbuf = base + K::kOffX, zbuf = base + K::kOffZ;
         const int64_t tok0 = u.start + u.c0 * kQ, ys = (int64_t)p.H * P;
-        const uint32_t ystep = (uint32_t)ys * (uint32_t)sizeof(T);
+        // Copies of 128 channels (those of absent heads left out) of a chunk's tokens, from token -3 on for x, to
+        // shared memory, 16 bytes at a time; behind the end of the sequence its last token is taken again.
+        constexpr int PIECES = K::kRow / 16, STEP = kWorkers / PIECES; // a thread keeps its piece of the rows
+        constexpr int ELS = 16 / (int)sizeof(T);
+        const int piece = me % PIECES, first = me / PIECES;
+        const bool mine = piece < u.nh * (P * (int)sizeof(T) / 16);
+        const int col = u.h0 * P + piece * ELS;
+        const uint32_t to = first * K::kRow + 16 * piece;
+        auto copy = [&](uint32_t buf, const T *rows, int64_t stride, int t, int tokens, bool before) { // tokens t, t + STEP, ..
+            const T *at = rows + t * stride;
+            // (tokens before the first chunk: copied by the caller)
+#pragma unroll
+            for (int i = 0; i < (kQ + STEP - 1) / STEP + 1; ++i)
+                if (t + i * STEP < kQ && (i > 0 || t >= 0 || before))
+                    cp_async16(buf + to + i * STEP * K::kRow, t + i * STEP < tokens ? at + i * STEP * stride : rows + (tokens - 1) * stride, false);
+        };
+        auto copy_z = [&](int c) {
+            const int64_t t0 = tok0 + (int64_t)c * kQ;
+            if (mine)
+                copy(zbuf, reinterpret_cast<const T *>(p.z) + t0 * p.z_stride + col, p.z_stride, first,
+                     (int)(u.end - t0 < kQ ? u.end - t0 : kQ), true);
+        };
+        auto copy_x = [&](int c) {
+            const int64_t t0 = tok0 + (int64_t)c * kQ;
+            const T *rows = reinterpret_cast<const T *>(p.xbc) + t0 * p.xbc_stride + col;
+            if (mine)
+                copy(xbuf, rows, p.xbc_stride, first - 3, (int)(u.end - t0 < kQ ? u.end - t0 : kQ), c > 0);
+            if (mine && c == 0 && first < 3) { // before the segment: the window, or the rows of the segment ahead
+                const T *row_before = conv_row<T>(p, u.n, u.start, t0 + first - 3);
+                cp_async16(xbuf + to, row_before == nullptr ? rows : row_before + col, row_before == nullptr);
+            }
+        };
         if (u.nc > 0)
-            copy_rows(xbuf, p.xbc, p.xbc_stride, tok0, 0, -3, me, kWorkers);
+            copy_x(0);
         float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f;
         if (live) { // times -log2(e), as the exponential of the SiLU takes its argument
             const float4 w = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + chan);
@@ -761,38 +771,32 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             const int64_t t0 = tok0 + (int64_t)c * kQ; // of chunk c
             // -- x of chunk c + 1: tokens 16 part ..
             cp_async_wait();
-            group_sync(1, kWorkers); // its rows have landed, and z of chunk c - 1 has been read
-            f2 x[8];
+            group_sync(1, kWorkers); // its rows have landed, and the output of chunk c - 1 has left shared memory
+            float x[16];
             if (more) {
                 if (!SUMMARY && c >= 0 && p.z != nullptr)
-                    copy_rows(zbuf, p.z, p.z_stride, t0, 1, 0, me, kWorkers);
-                float r[20]; // tokens -4 (unused), -3, .., 15
+                    copy_z(c);
+                float r[19]; // tokens -3, .., 15
                 const T *src = reinterpret_cast<const T *>(sm + K::kOffX) + (16 * part) * 128 + row;
-                r[0] = 0.f;
 #pragma unroll
-                for (int t = 1; t < 20; ++t)
-                    r[t] = to_f(src[(t - 1) * 128]);
+                for (int t = 0; t < 19; ++t)
+                    r[t] = to_f(src[t * 128]);
                 group_sync(1, kWorkers); // every thread has its tokens
                 if (c + 2 < u.nc)
-                    copy_rows(xbuf, p.xbc, p.xbc_stride, t0 + 2 * kQ, c + 2, -3, me, kWorkers);
-                const f2 p1 = pack(w1, w1), p3 = pack(w3, w3), pb = pack(wb, wb);
+                    copy_x(c + 2);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) { // tokens 2 t, 2 t + 1; taps 1 and 3 sit in register pairs
-                    const float *v = r + 2 * t;
-                    const float2 m = unpack(fma2(p3, pack(v[4], v[5]), fma2(p1, pack(v[2], v[3]), pb)));
-                    x[t] = pack(silu_scaled(fmaf(w2, v[3], fmaf(w0, v[1], m.x))), silu_scaled(fmaf(w2, v[4], fmaf(w0, v[2], m.y))));
-                }
+                for (int t = 0; t < 16; ++t)
+                    x[t] = silu_scaled(fmaf(w3, r[t + 3], fmaf(w2, r[t + 2], fmaf(w1, r[t + 1], fmaf(w0, r[t], wb)))));
                 const int valid = live ? (int)(u.end - t0 - kQ < kQ ? u.end - t0 - kQ : kQ) - 16 * part : 0;
                 if (valid < 16) {
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const float2 v = unpack(x[t]);
-                        x[t] = pack(2 * t < valid ? v.x : 0.f, 2 * t + 1 < valid ? v.y : 0.f);
-                    }
+                    for (int t = 0; t < 16; ++t)
+                        if (t >= valid)
+                            x[t] = 0.f;
                 }
             } else {
                 if (!SUMMARY && c >= 0 && p.z != nullptr)
-                    copy_rows(zbuf, p.z, p.z_stride, t0, 1, 0, me, kWorkers);
+                    copy_z(c);
             }
             // -- the state entering chunk c + 1, and x' of that chunk
             if (c >= 0) {
@@ -817,20 +821,22 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     for (int i = 0; i < CW; i += 16) {
                         uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            split2(h[i / 2 + k], hi[k], lo[k]);
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 v = unpack(h[i / 2 + k]);
+                            split2(v.x, v.y, hi[k], lo[k]);
+                        }
                         tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
                         tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
                     }
                 }
                 ok = ok && gate_ready(c + 1);
-                const ulonglong2 *wt = reinterpret_cast<const ulonglong2 *>(gate[(c + 1) % K::kGateSlots][hl] + 192 + 16 * part);
+                const float4 *wt = reinterpret_cast<const float4 *>(gate[(c + 1) % K::kGateSlots][hl] + 192 + 16 * part);
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
-                    const ulonglong2 w = wt[k / 2];
-                    split2(mul2(x[k], w.x), hi[k], lo[k]);
-                    split2(mul2(x[k + 1], w.y), hi[k + 1], lo[k + 1]);
+                    const float4 w = wt[k / 2];
+                    split2(x[2 * k] * w.x, x[2 * k + 1] * w.y, hi[k], lo[k]);
+                    split2(x[2 * k + 2] * w.z, x[2 * k + 3] * w.w, hi[k + 1], lo[k + 1]);
                 }
                 tmem_st8(tmem + lanes + K::kXP + 8 * part, hi);
                 tmem_st8(tmem + lanes + K::kXP + 32 + 8 * part, lo);
@@ -844,52 +850,46 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 continue;
             }
             // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
-            f2 y[8];
+            float y[16];
             if (c >= 0) {
                 ok = ok && i_done(c);
                 tc_fence_after();
-                float v[16], e[16];
-                tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + 16 * part, v);
+                float e[16];
+                tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + 16 * part, y);
                 tmem_ld16(tmem + lanes + K::kYA + 64 * hl + 16 * part, e);
                 tmem_wait_ld();
-                const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[c % K::kGateSlots][hl] + 256 + 16 * part);
+                const float4 *eg = reinterpret_cast<const float4 *>(gate[c % K::kGateSlots][hl] + 256 + 16 * part);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const ulonglong2 f = eg[k];
-                    y[2 * k] = fma2(f.x, pack(v[4 * k], v[4 * k + 1]), pack(e[4 * k], e[4 * k + 1]));
-                    y[2 * k + 1] = fma2(f.y, pack(v[4 * k + 2], v[4 * k + 3]), pack(e[4 * k + 2], e[4 * k + 3]));
+                    const float4 f = eg[k];
+                    y[4 * k] = fmaf(f.x, y[4 * k], e[4 * k]);
+                    y[4 * k + 1] = fmaf(f.y, y[4 * k + 1], e[4 * k + 1]);
+                    y[4 * k + 2] = fmaf(f.z, y[4 * k + 2], e[4 * k + 2]);
+                    y[4 * k + 3] = fmaf(f.w, y[4 * k + 3], e[4 * k + 3]);
                 }
                 arrive(kGEmpty + c % K::kGateSlots);
             }
             if (more) {
                 // A non-finite x would reach the tokens before it in its chunk (as 0 times it): the
                 // product takes 0 instead, and the output is set from that token on.
-                f2 zero2 = 0ull;
+                float zero = 0.f;
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    zero2 = fma2(x[t], 0ull, zero2);
+                for (int t = 0; t < 16; ++t)
+                    zero = fmaf(x[t], 0.f, zero);
                 int first = kQ;
-                const float2 z = unpack(zero2);
-                if (z.x + z.y != 0.f) {
+                if (zero != 0.f) {
 #pragma unroll
-                    for (int t = 7; t >= 0; --t) {
-                        float2 v = unpack(x[t]);
-                        if (!(fabsf(v.y) <= 3.402823466e38f)) {
-                            first = 16 * part + 2 * t + 1;
-                            v.y = 0.f;
+                    for (int t = 15; t >= 0; --t)
+                        if (!(fabsf(x[t]) <= 3.402823466e38f)) {
+                            first = 16 * part + t;
+                            x[t] = 0.f;
                         }
-                        if (!(fabsf(v.x) <= 3.402823466e38f)) {
-                            first = 16 * part + 2 * t;
-                            v.x = 0.f;
-                        }
-                        x[t] = pack(v.x, v.y);
-                    }
                 }
                 bad[(c + 1) & 1][row][part] = (uint8_t)first;
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    split2(x[k], hi[k], lo[k]);
+                    split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
                 tmem_st8(tmem + lanes + K::kX + 8 * part, hi);
                 tmem_st8(tmem + lanes + K::kX + 32 + 8 * part, lo);
                 tmem_wait_st();
@@ -905,32 +905,33 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 for (int k = 0; k <= part; ++k)
                     first = min(first, (int)bad[c & 1][row][k]);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const float2 v = unpack(y[t]);
-                    const float nan = __uint_as_float(0x7fffffffu);
-                    y[t] = pack(16 * part + 2 * t >= first ? nan : v.x, 16 * part + 2 * t + 1 >= first ? nan : v.y);
-                }
+                for (int t = 0; t < 16; ++t)
+                    if (16 * part + t >= first)
+                        y[t] = __uint_as_float(0x7fffffffu);
             }
+            // through shared memory, over z where there is one: 16 bytes of a row per store (2-byte stores
+            // of a channel each took 3400 cycles a chunk)
+            T *yr = reinterpret_cast<T *>(smem_raw + (base - smem_u32(smem_raw)) + K::kOffZ) + (16 * part) * 128 + row;
             if (p.z != nullptr) {
                 cp_async_wait();
                 group_sync(1, kWorkers); // z of this chunk has landed
-                const T *zr = reinterpret_cast<const T *>(sm + K::kOffZ) + (16 * part) * 128 + row;
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    y[t] = mul2(y[t], pack(silu(to_f(zr[2 * t * 128])), silu(to_f(zr[(2 * t + 1) * 128]))));
+                for (int t = 0; t < 16; ++t)
+                    y[t] *= silu(to_f(yr[t * 128]));
             }
-            // 32-bit byte offsets from the chunk's first row: at most 64 H P elements
-            char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + t0 * ys + u.h0 * P);
-            uint32_t at = row * (uint32_t)sizeof(T) + 16 * part * ystep;
-            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part : 0;
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const float2 v = unpack(y[t]);
-                if (2 * t < valid)
-                    *reinterpret_cast<T *>(dst + at) = from_f<T>(v.x);
-                if (2 * t + 1 < valid)
-                    *reinterpret_cast<T *>(dst + (at + ystep)) = from_f<T>(v.y);
-                at += 2 * ystep;
+            for (int t = 0; t < 16; t += 2)
+                put2(yr + t * 128, yr + (t + 1) * 128, y[t], y[t + 1]);
+            group_sync(1, kWorkers);
+            if (mine) {
+                const int tokens = (int)(u.end - t0 < kQ ? u.end - t0 : kQ);
+                T *dst = reinterpret_cast<T *>(p.y) + (t0 + first) * ys + col;
+#pragma unroll
+                for (int i = 0; i < kQ / STEP; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sm + K::kOffZ + to + i * STEP * K::kRow);
+                    if (first + i * STEP < tokens)
+                        *reinterpret_cast<uint4 *>(dst + i * STEP * ys) = v;
+                }
             }
         }
         cp_async_wait();
@@ -1010,7 +1011,7 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
         e = cudaFuncSetAttribute(ssm_prep_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem<S>());
         if (e != cudaSuccess)
             return e;
-        ssm_prep_kernel<T, S><<<dim3((unsigned)chunks, p.G), kPrepThreads, prep_smem<S>(), s>>>(
+        ssm_prep_kernel<T, S><<<dim3((unsigned)chunks, p.G, 2), kPrepThreads, prep_smem<S>(), s>>>(
             p, (__nv_bfloat16 *)(ws + l.bc), (float *)(ws + l.cb), (float *)(ws + l.gates), status);
         e = record_if(begin, s);
         if (e != cudaSuccess)
