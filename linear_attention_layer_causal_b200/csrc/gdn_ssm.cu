@@ -689,33 +689,42 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         // Copies of 128 channels (those of absent heads left out) of a chunk's tokens, from token -3 on for x, to
         // shared memory, 16 bytes at a time; behind the end of the sequence its last token is taken again.
         constexpr int PIECES = K::kRow / 16, STEP = kWorkers / PIECES; // a thread keeps its piece of the rows
-        constexpr int ELS = 16 / (int)sizeof(T);
         const int piece = me % PIECES, first = me / PIECES;
         const bool mine = piece < u.nh * (P * (int)sizeof(T) / 16);
-        const int col = u.h0 * P + piece * ELS;
         const uint32_t to = first * K::kRow + 16 * piece;
-        auto copy = [&](uint32_t buf, const T *rows, int64_t stride, int t, int tokens, bool before) { // tokens t, t + STEP, ..
-            const T *at = rows + t * stride;
-            // (tokens before the first chunk: copied by the caller)
+        const int64_t xrow = p.xbc_stride * (int64_t)sizeof(T), zrow = p.z_stride * (int64_t)sizeof(T);
+        const char *xat = reinterpret_cast<const char *>(p.xbc) + (tok0 + first - 3) * xrow + u.h0 * P * (int)sizeof(T) + 16 * piece;
+        const char *zat = reinterpret_cast<const char *>(p.z) + (tok0 + first) * zrow + u.h0 * P * (int)sizeof(T) + 16 * piece;
+        auto copy_z = [&](int c) { // chunks in turn: zat is this thread's first row of the next one
+            if (mine) {
+                const int tokens = (int)(u.end - tok0 < (int64_t)(c + 1) * kQ ? u.end - tok0 - (int64_t)c * kQ : kQ);
 #pragma unroll
-            for (int i = 0; i < (kQ + STEP - 1) / STEP + 1; ++i)
-                if (t + i * STEP < kQ && (i > 0 || t >= 0 || before))
-                    cp_async16(buf + to + i * STEP * K::kRow, t + i * STEP < tokens ? at + i * STEP * stride : rows + (tokens - 1) * stride, false);
+                for (int i = 0; i < kQ / STEP; ++i) {
+                    const int t = first + i * STEP;
+                    cp_async16(zbuf + to + i * STEP * K::kRow, zat + (t < tokens ? i * STEP : tokens - 1 - first) * zrow, false);
+                }
+                zat += kQ * zrow;
+            }
         };
-        auto copy_z = [&](int c) {
-            const int64_t t0 = tok0 + (int64_t)c * kQ;
-            if (mine)
-                copy(zbuf, reinterpret_cast<const T *>(p.z) + t0 * p.z_stride + col, p.z_stride, first,
-                     (int)(u.end - t0 < kQ ? u.end - t0 : kQ), true);
-        };
-        auto copy_x = [&](int c) {
-            const int64_t t0 = tok0 + (int64_t)c * kQ;
-            const T *rows = reinterpret_cast<const T *>(p.xbc) + t0 * p.xbc_stride + col;
-            if (mine)
-                copy(xbuf, rows, p.xbc_stride, first - 3, (int)(u.end - t0 < kQ ? u.end - t0 : kQ), c > 0);
-            if (mine && c == 0 && first < 3) { // before the segment: the window, or the rows of the segment ahead
-                const T *row_before = conv_row<T>(p, u.n, u.start, t0 + first - 3);
-                cp_async16(xbuf + to, row_before == nullptr ? rows : row_before + col, row_before == nullptr);
+        auto copy_x = [&](int c) { // likewise, from token -3 on
+            if (mine) {
+                const int tokens = (int)(u.end - tok0 < (int64_t)(c + 1) * kQ ? u.end - tok0 - (int64_t)c * kQ : kQ);
+#pragma unroll
+                for (int i = 0; i < kQ / STEP + 1; ++i) {
+                    const int t = first - 3 + i * STEP;
+                    if (i < kQ / STEP || t < kQ) {
+                        const char *at = xat + (t < tokens ? i * STEP : tokens + 2 - first) * xrow;
+                        bool zeros = false;
+                        if (i == 0 && t < 0 && c == 0) { // before the segment: the window, or the rows of the segment ahead
+                            const T *before = conv_row<T>(p, u.n, u.start, tok0 + t);
+                            zeros = before == nullptr;
+                            at = zeros ? reinterpret_cast<const char *>(p.conv_w)
+                                       : reinterpret_cast<const char *>(before + u.h0 * P) + 16 * piece;
+                        }
+                        cp_async16(xbuf + to + i * STEP * K::kRow, at, zeros);
+                    }
+                }
+                xat += kQ * xrow;
             }
         };
         if (u.nc > 0)
@@ -781,9 +790,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
                 for (int t = 0; t < 19; ++t)
                     r[t] = to_f(src[t * 128]);
-                group_sync(1, kWorkers); // every thread has its tokens
-                if (c + 2 < u.nc)
-                    copy_x(c + 2);
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     x[t] = silu_scaled(fmaf(w3, r[t + 3], fmaf(w2, r[t + 2], fmaf(w1, r[t + 1], fmaf(w0, r[t], wb)))));
@@ -800,7 +806,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             }
             // -- the state entering chunk c + 1, and x' of that chunk
             if (c >= 0) {
-                ok = ok && gate_ready(c) && wait_all(kUDone, c & 1);
+                ok = ok && wait_all(kUDone, c & 1); // (the gates were waited for as the next chunk's)
                 tc_fence_after();
                 const float gamma = live ? gate[c % K::kGateSlots][hl][256 + 63] : 0.f;
                 decay *= gamma;
@@ -847,6 +853,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             if (SUMMARY) {
                 if (c >= 0)
                     arrive(kGEmpty + c % K::kGateSlots);
+                if (c + 2 < u.nc) {
+                    group_sync(1, kWorkers); // every thread has its tokens
+                    copy_x(c + 2);
+                }
                 continue;
             }
             // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
@@ -896,6 +906,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 tc_fence_before();
                 arrive(kXFull);
             }
+            // the tokens of chunk c + 1 are in every thread's registers, and z of chunk c has landed
+            cp_async_wait();
+            group_sync(1, kWorkers);
+            if (c + 2 < u.nc)
+                copy_x(c + 2);
             if (c < 0)
                 continue;
             // -- the output of chunk c: gate and store
@@ -909,12 +924,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     if (16 * part + t >= first)
                         y[t] = __uint_as_float(0x7fffffffu);
             }
-            // through shared memory, over z where there is one: 16 bytes of a row per store (2-byte stores
-            // of a channel each took 3400 cycles a chunk)
+            // through shared memory, over z where there is one, so that a warp stores its 32 channels of 8 tokens
+            // at a time (2-byte stores of a channel took 3400 cycles a chunk)
             T *yr = reinterpret_cast<T *>(smem_raw + (base - smem_u32(smem_raw)) + K::kOffZ) + (16 * part) * 128 + row;
             if (p.z != nullptr) {
-                cp_async_wait();
-                group_sync(1, kWorkers); // z of this chunk has landed
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     y[t] *= silu(to_f(yr[t * 128]));
@@ -922,15 +935,18 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
             for (int t = 0; t < 16; t += 2)
                 put2(yr + t * 128, yr + (t + 1) * 128, y[t], y[t + 1]);
-            group_sync(1, kWorkers);
-            if (mine) {
-                const int tokens = (int)(u.end - t0 < kQ ? u.end - t0 : kQ);
-                T *dst = reinterpret_cast<T *>(p.y) + (t0 + first) * ys + col;
+            __syncwarp();
+            if (live) {
+                constexpr int LANES = 2 * (int)sizeof(T), ROWS = 32 / LANES; // lanes of a row's 32 channels, rows at once
+                const int valid = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part;
+                const int t = lane / LANES, k = lane % LANES;
+                const uint8_t *from = sm + K::kOffZ + (16 * part + t) * K::kRow + 32 * q * (int)sizeof(T) + 16 * k;
+                char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + (t0 + 16 * part + t) * ys + u.h0 * P + 32 * q) + 16 * k;
 #pragma unroll
-                for (int i = 0; i < kQ / STEP; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(sm + K::kOffZ + to + i * STEP * K::kRow);
-                    if (first + i * STEP < tokens)
-                        *reinterpret_cast<uint4 *>(dst + i * STEP * ys) = v;
+                for (int i = 0; i < 16; i += ROWS) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(from + i * K::kRow);
+                    if (t + i < valid)
+                        *reinterpret_cast<uint4 *>(dst + i * ys * (int64_t)sizeof(T)) = v;
                 }
             }
         }
