@@ -126,7 +126,7 @@ template <typename T> __device__ __forceinline__ const T *conv_row(const SsmArgs
 
 // ------------------------------------------------------------------- prep
 
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 512;
 template <int S> constexpr size_t prep_smem() { return (size_t)4 * kQ * (S + 8) * 2; }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -147,7 +147,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // products C_t . B_s of s's and t's 16-blocks with s <= t, and a gate record
 // for each head of the group.
 template <typename T, int S>
-__global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p, __nv_bfloat16 *bc, float *cb, float *gates,
+__global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs p, __nv_bfloat16 *bc, float *cb, float *gates,
                                                                 uint32_t *status) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int LDS = S + 8; // row length in shared memory: rows 16 bytes apart in banks
@@ -275,35 +275,31 @@ __global__ void __launch_bounds__(kPrepThreads) ssm_prep_kernel(const SsmArgs p,
 
     __syncthreads();
 
-    // C B^T: warp w has rows 16 (w % 4) .., columns 32 (w / 4) ..
-    const int mt = warp & 3, nh = warp >> 2;
-    if (2 * nh <= mt) {
-        float acc[4][4] = {};
+    // C B^T: warp w has rows 16 (w % 4) .., columns 16 (w / 4) ..
+    const int mt = warp & 3, nt = warp >> 2;
+    if (nt <= mt) {
+        float acc[2][4] = {};
         const uint32_t arow = (uint32_t)((mt * 16 + (lane & 15)) * LDS + (lane >> 4) * 8) * 2;
-        const uint32_t brow = (uint32_t)((nh * 32 + (lane & 7) + (lane >> 4) * 8) * LDS + ((lane >> 3) & 1) * 8) * 2;
+        const uint32_t brow = (uint32_t)((nt * 16 + (lane & 7) + (lane >> 4) * 8) * LDS + ((lane >> 3) & 1) * 8) * 2;
         const uint32_t sb = smem_u32(smem);
         constexpr uint32_t PART = kQ * LDS * 2;
 #pragma unroll
         for (int k = 0; k < S; k += 16) {
-            uint32_t ah[4], al[4];
+            uint32_t ah[4], al[4], bh[4], bl[4];
             ldmatrix4(ah, sb + 2 * PART + arow + 2 * k);
             ldmatrix4(al, sb + 3 * PART + arow + 2 * k);
+            ldmatrix4(bh, sb + brow + 2 * k);
+            ldmatrix4(bl, sb + PART + brow + 2 * k);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) { // 16 columns at a time
-                uint32_t bh[4], bl[4];
-                ldmatrix4(bh, sb + brow + j * 16 * LDS * 2 + 2 * k);
-                ldmatrix4(bl, sb + PART + brow + j * 16 * LDS * 2 + 2 * k);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mma_bf16(acc[2 * j + i], ah, bh[2 * i], bh[2 * i + 1]);
-                    mma_bf16(acc[2 * j + i], ah, bl[2 * i], bl[2 * i + 1]);
-                    mma_bf16(acc[2 * j + i], al, bh[2 * i], bh[2 * i + 1]);
-                }
+            for (int i = 0; i < 2; ++i) {
+                mma_bf16(acc[i], ah, bh[2 * i], bh[2 * i + 1]);
+                mma_bf16(acc[i], ah, bl[2 * i], bl[2 * i + 1]);
+                mma_bf16(acc[i], al, bh[2 * i], bh[2 * i + 1]);
             }
         }
-        float *out = cb + (id * p.G + g) * (kQ * kQ) + (mt * 16 + (lane >> 2)) * kQ + nh * 32 + 2 * (lane & 3);
+        float *out = cb + (id * p.G + g) * (kQ * kQ) + (mt * 16 + (lane >> 2)) * kQ + nt * 16 + 2 * (lane & 3);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             *reinterpret_cast<float2 *>(out + 8 * j) = make_float2(acc[j][0], acc[j][1]);
             *reinterpret_cast<float2 *>(out + 8 * kQ + 8 * j) = make_float2(acc[j][2], acc[j][3]);
         }
@@ -352,10 +348,10 @@ template <typename T, int P, int S> struct Scan {
     static constexpr int kMBufs = sizeof(T) == 2 ? 2 : 1;
     static constexpr int kCbBytes = kQ * kQ * 4;
     static constexpr int kRow = 128 * sizeof(T);      // 128 channels of a token
-    static constexpr int kXBytes = (kQ + 3) * kRow, kZBytes = kQ * kRow;
+    static constexpr int kXBytes = (kQ + 3) * kRow;   // x; and z, or the next x
     static constexpr int kOffM = kSlots * kHalf, kOffCb = kOffM + kMBufs * kMBytes, kOffX = kOffCb + kCbBytes,
                          kOffZ = kOffX + kXBytes;
-    static constexpr size_t kSmem = 1024 + kOffZ + kZBytes;
+    static constexpr size_t kSmem = 1024 + kOffZ + kXBytes;
     // TMEM columns
     static constexpr uint32_t kDH = 0;             // x' B^T, then H hi and lo of the next chunk
     static constexpr uint32_t kYI = 128;           // H C^T
@@ -409,6 +405,8 @@ struct ScanArgs {
 // The `n` threads of some warpgroups (named barrier `id`).
 __device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 // Warpgroup 0: a warp that loads, a warp that issues the MMAs, two that make M.
 // The other four work in step, each on 16 tokens of a chunk and a quarter of
@@ -474,8 +472,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     // A wait that runs out (about a second) makes every role stop at its next
     // wait; what is in flight is waited for before the block ends.
-    auto wait = [&](int i, uint32_t parity) {
+    auto wait = [&](int i, uint32_t parity, bool patient = false) {
         bool ok = mbar_test_wait(bar(i), parity);
+        // the loads and M run ahead: they ask now and then, and leave the schedulers to the others
+        for (int k = 0; patient && !ok && k < 16; ++k) {
+            __nanosleep(200);
+            ok = mbar_test_wait(bar(i), parity);
+        }
         if (!ok)
             ok = !*abort_v && mbar_wait_sleeping(bar(i), parity, kDefaultWaitLimit);
         if (!ok) {
@@ -484,14 +487,14 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         }
         return ok;
     };
-    auto wait_all = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)); };
+    auto wait_all = [&](int i, uint32_t parity, bool patient = false) { return __all_sync(0xffffffffu, wait(i, parity, patient)); };
     auto arrive = [&](int i) { // by a warp
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bar(i));
     };
-    auto gate_ready = [&](int c) { return wait_all(kGFull + c % K::kGateSlots, (c / K::kGateSlots) & 1); };
-    auto i_done = [&](int c) { return wait_all(kIDone + (c & 1), (c >> 1) & 1); };
+    auto gate_ready = [&](int c, bool patient = false) { return wait_all(kGFull + c % K::kGateSlots, (c / K::kGateSlots) & 1, patient); };
+    auto i_done = [&](int c, bool patient = false) { return wait_all(kIDone + (c & 1), (c >> 1) & 1, patient); };
     const int row = 32 * q + lane;          // state row of a thread of the X, S, Y warpgroups
     const int hl = P == 64 ? q >> 1 : 0;    // its head within the block (uniform over the warp)
     const bool live = hl < u.nh;
@@ -508,13 +511,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 bool ok = true;
                 for (int c = 0; ok && c < u.nc; ++c) {
                     const int gs = c % K::kGateSlots;
-                    if (!(ok = wait(kGEmpty + gs, ((c / K::kGateSlots) & 1) ^ 1)))
+                    if (!(ok = wait(kGEmpty + gs, ((c / K::kGateSlots) & 1) ^ 1, true)))
                         break;
                     mbar_arrive_expect_tx(bar(kGFull + gs), gbytes);
                     bulk_load(smem_u32(gate[gs]), a.gates + ((id0 + c) * p.H + u.h0) * kGateRec, gbytes, bar(kGFull + gs));
                     const int y = (int)(((id0 + c) * p.G + u.g) * kQ);
                     if (!SUMMARY) {
-                        if (!(ok = wait(kCbEmpty, (c & 1) ^ 1))) {
+                        if (!(ok = wait(kCbEmpty, (c & 1) ^ 1, true))) {
                             mbar_wait_bounded(bar(kGFull + gs), (c / K::kGateSlots) & 1, kDefaultWaitLimit);
                             break;
                         }
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         tma_load_2d(base + K::kOffCb + 8192, &tcb, 32, y, bar(kCbFull));
                     }
                     for (int part = SUMMARY ? 1 : 0; part < 2; ++part) { // C (channels 2 S ..), then B
-                        if (!(ok = wait(kBcEmpty + slot, ph))) {
+                        if (!(ok = wait(kBcEmpty + slot, ph, true))) {
                             mbar_wait_bounded(bar(kGFull + gs), (c / K::kGateSlots) & 1, kDefaultWaitLimit);
                             if (!SUMMARY)
                                 mbar_wait_bounded(bar(kCbFull), c & 1, kDefaultWaitLimit);
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
                 const int mb = c % K::kMBufs, gs = c % K::kGateSlots;
                 // the chunk that last had this buffer: its products are done
-                if (!gate_ready(c) || !wait_all(kCbFull, c & 1) || (c >= K::kMBufs && !i_done(c - K::kMBufs)))
+                if (!gate_ready(c, true) || !wait_all(kCbFull, c & 1, true) || (c >= K::kMBufs && !i_done(c - K::kMBufs, true)))
                     break;
                 const uint32_t mbuf = base + K::kOffM + mb * K::kMBytes;
                 // 16-blocks (row, column): (0, 0) (3, 0) (3, 1) (3, 2) (3, 3) of one warp, (1, 0) (1, 1) (2, 0)
@@ -684,7 +687,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int part = wg - 1, me = tid - 128;
-        const uint32_t xbuf = base + K::kOffX, zbuf = base + K::kOffZ;
+        // the summary pass has no z: its room is a second buffer for x
+        auto xoff = [&](int c) { return SUMMARY && (c & 1) ? K::kOffZ : K::kOffX; };
+        const uint32_t zbuf = base + K::kOffZ;
         const int64_t tok0 = u.start + u.c0 * kQ, ys = (int64_t)p.H * P;
         // Copies of 128 channels (those of absent heads left out) of a chunk's tokens, from token -3 on for x, to
         // shared memory, 16 bytes at a time; behind the end of the sequence its last token is taken again.
@@ -721,7 +726,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             at = zeros ? reinterpret_cast<const char *>(p.conv_w)
                                        : reinterpret_cast<const char *>(before + u.h0 * P) + 16 * piece;
                         }
-                        cp_async16(xbuf + to + i * STEP * K::kRow, at, zeros);
+                        cp_async16(base + xoff(c) + to + i * STEP * K::kRow, at, zeros);
                     }
                 }
                 xat += kQ * xrow;
@@ -729,6 +734,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         };
         if (u.nc > 0)
             copy_x(0);
+        cp_async_commit();
+        if (SUMMARY && u.nc > 1)
+            copy_x(1);
+        cp_async_commit();
         float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f;
         if (live) { // times -log2(e), as the exponential of the SiLU takes its argument
             const float4 w = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + chan);
@@ -779,17 +788,26 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             const bool more = c + 1 < u.nc;
             const int64_t t0 = tok0 + (int64_t)c * kQ; // of chunk c
             // -- x of chunk c + 1: tokens 16 part ..
-            cp_async_wait();
+            if (SUMMARY)
+                cp_async_wait_but_one(); // (the chunk after it is on its way)
+            else
+                cp_async_wait();
             group_sync(1, kWorkers); // its rows have landed, and the output of chunk c - 1 has left shared memory
             float x[16];
             if (more) {
                 if (!SUMMARY && c >= 0 && p.z != nullptr)
                     copy_z(c);
                 float r[19]; // tokens -3, .., 15
-                const T *src = reinterpret_cast<const T *>(sm + K::kOffX) + (16 * part) * 128 + row;
+                const T *src = reinterpret_cast<const T *>(sm + xoff(c + 1)) + (16 * part) * 128 + row;
 #pragma unroll
                 for (int t = 0; t < 19; ++t)
                     r[t] = to_f(src[t * 128]);
+                if (SUMMARY) {
+                    group_sync(1, kWorkers); // every thread has its tokens
+                    if (c + 3 < u.nc)
+                        copy_x(c + 3);
+                    cp_async_commit();
+                }
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     x[t] = silu_scaled(fmaf(w3, r[t + 3], fmaf(w2, r[t + 2], fmaf(w1, r[t + 1], fmaf(w0, r[t], wb)))));
@@ -853,10 +871,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             if (SUMMARY) {
                 if (c >= 0)
                     arrive(kGEmpty + c % K::kGateSlots);
-                if (c + 2 < u.nc) {
-                    group_sync(1, kWorkers); // every thread has its tokens
-                    copy_x(c + 2);
-                }
                 continue;
             }
             // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
