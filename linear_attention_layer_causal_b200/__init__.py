@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import cached_property
 
@@ -551,35 +552,24 @@ def _rows(name, t, shape, dtype, device, optional=False):
     return t.data_ptr(), strides[0] if shape[0] > 1 else n
 
 
-class _on:
-    """Makes the tensors' device current and gives the stream to launch on: that device's current
-    one, or the caller's, which then also owns what is allocated inside (a temporary workspace must
-    not return to another stream's pool while a kernel uses it)."""
-
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError("tensors passed to the library must live on a CUDA device")
-        if stream is not None and stream.device != device:
+def _on(device, stream):
+    """(stream handle, context): the stream to launch on is that device's current one, or the
+    caller's, which then also owns what is allocated in the context (a temporary workspace must
+    not return to another stream's pool while a kernel uses it); the context makes the tensors'
+    device the current one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("tensors passed to the library must live on a CUDA device")
+    if stream is not None:
+        if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.guard = None
-        if stream is not None:
-            self.guard = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-            stream = torch.cuda.current_stream(device)
-        else:
-            stream = torch.cuda.current_stream()
-        self.stream = stream.cuda_stream
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    if torch.cuda.current_device() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index), _HERE_AND_NOW
+    return torch.cuda.current_stream(device).cuda_stream, torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
 
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+_HERE_AND_NOW = nullcontext()
 
 
 def _workspace(workspace, need, device):
@@ -624,7 +614,8 @@ def ssm_prefill(cfg: SsmConfig, xbc, dt, cu_seqlens, conv_w, A_log, *, conv_b=No
     import torch
     N, B, dev, act = xbc.shape[0], cu_seqlens.shape[0] - 1, xbc.device, _act(cfg)
     H, P, S, C = cfg.num_heads, cfg.head_dim, cfg.state_dim, cfg.conv_dim
-    with _on(dev, stream) as s:
+    s, on = _on(dev, stream)
+    with on:
         xp, xs = _rows("xbc", xbc, (N, C), act, dev)
         dp, ds = _rows("dt", dt, (N, H), act, dev)
         zp, zs = _rows("z", z, (N, H, P), act, dev, optional=True)
@@ -661,7 +652,8 @@ def ssm_decode(cfg: SsmConfig, xbc, dt, state, conv_cache, conv_w, A_log, *, con
     import torch
     B, dev, act = xbc.shape[0], xbc.device, _act(cfg)
     H, P, S, C = cfg.num_heads, cfg.head_dim, cfg.state_dim, cfg.conv_dim
-    with _on(dev, stream) as s:
+    s, on = _on(dev, stream)
+    with on:
         xp, xs = _rows("xbc", xbc, (B, C), act, dev)
         dp, ds = _rows("dt", dt, (B, H), act, dev)
         zp, zs = _rows("z", z, (B, H, P), act, dev, optional=True)
@@ -690,7 +682,8 @@ def _norm_call(x, weight, residual, groups, eps, weight_offset, q, scale, residu
     shape, dev, act = x.shape, x.device, x.dtype
     rows, dim = shape
     blocks = (rows, -(-dim // BLOCK))
-    with _on(dev, stream) as s:
+    s, on = _on(dev, stream)
+    with on:
         xp, xs = _rows("x", x, shape, act, dev)
         if q is None:
             q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
@@ -756,7 +749,8 @@ def matmul_fp8(a, a_scale, w, w_scale, *, out_dtype=None, out=None, workspace=No
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     kb, f8 = -(-K // BLOCK), torch.float8_e4m3fn
-    with _on(dev, stream) as s:
+    s, on = _on(dev, stream)
+    with on:
         ap, wp = _check("a", a, (M, K), f8, dev), _check("w", w, (N, K), f8, dev)
         sa = _check("a_scale", a_scale, (M, kb), torch.float32, dev, False)
         sw = _check("w_scale", w_scale, (-(-N // BLOCK), kb), torch.float32, dev, False)

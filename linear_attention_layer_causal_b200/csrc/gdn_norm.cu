@@ -15,21 +15,27 @@
 namespace gdn {
 namespace {
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8]) {
-    const Vec16<__nv_bfloat16> x = ld16(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = x.get(i);
-}
-template <> __device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
-    const Vec16<float> x = ld16(p), y = ld16(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = x.get(i);
-        v[i + 4] = y.get(i);
+// Eight activations as loaded: 16 bytes of bf16 or 32 of float32.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w = i < 2 ? a.x : i < 4 ? a.y : i < 6 ? a.z : a.w;
+        return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
     }
-}
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        const float4 v = i < 4 ? a : b;
+        return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+    }
+};
 template <typename T> __device__ __forceinline__ void store8(T *p, const float (&v)[8]);
 template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *p, const float (&v)[8]) {
     Vec16<__nv_bfloat16> x;
@@ -51,36 +57,21 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// r of unit u of a row: x + residual in float32.
-template <typename T>
-__device__ __forceinline__ void load_unit(const T *x, const T *res, int u, float (&v)[8]) {
-    load8(x + 8 * u, v);
-    if (res != nullptr) {
-        float w[8];
-        load8(res + 8 * u, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] += w[i];
-    }
-}
-
 // The outputs of unit u (active), and its share of the block's maximum.  The
 // maximum is taken over the bit patterns of |v|, which order like the values
 // and put infinity and NaN above all of them, so that neither is lost.
 template <typename T>
 __device__ __forceinline__ void emit_unit(const NormArgs &p, bool active, int64_t row, int first, int u,
-                                          float rs, float (&v)[8]) {
+                                          float rs, const Raw8<float> &w, float (&v)[8]) {
     const int col = first + 8 * u; // column in the whole row
     const int64_t at = row * p.dim + col;
     if (active) {
         if (p.residual_out != nullptr)
             store8(reinterpret_cast<T *>(p.residual_out) + at, v);
         if (p.weight != nullptr) {
-            float w[8];
-            load8(p.weight + col, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = v[i] * rs * (p.weight_offset + w[i]);
+                v[i] = v[i] * rs * (p.weight_offset + w.get(i));
         }
         if (p.y != nullptr)
             store8(reinterpret_cast<T *>(p.y) + at, v);
@@ -110,73 +101,122 @@ __device__ __forceinline__ void emit_unit(const NormArgs &p, bool active, int64_
         p.scale[row * ((p.dim + 127) / 128) + col / 128] = scale;
 }
 
-// One row part (a norm group) per `TPR` threads, NU units per thread in
-// registers; NU = 0: parts of any length, read a second time for the output.
+// Row parts (norm groups) per `TPR` threads, NU units per thread in registers;
+// NU = 0: parts of any length, read a second time for the output.
+// With fewer blocks than parts a block takes every gridDim-th part: its
+// weights stay in registers (the host makes the step a multiple of the number
+// of groups), and the next part is on its way while this one is worked on.  At
+// 4096 x 8192 bf16 with a residual, a block per row took 59 us.
 template <typename T, int TPR, int NU>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormArgs p) {
-    constexpr int kThreads = TPR < 256 ? 256 : TPR;
-    __shared__ float red[kThreads / 32];
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T) == 2 ? 2 : 1) norm_kernel(const NormArgs p) {
+    constexpr int kThreads = TPR < 256 ? 256 : TPR, R = NU > 0 ? NU : 1;
+    __shared__ float red[2][kThreads / 32];
     const int tid = threadIdx.x % TPR;
-    const int64_t part = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
-    if (part >= p.rows * p.groups)
+    const int64_t parts = p.rows * p.groups, step = (int64_t)gridDim.x * (kThreads / TPR);
+    int64_t part = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+    if (part >= parts)
         return; // whole warps: TPR is a multiple of 32
-    const int64_t row = part / p.groups;
     const int len = p.dim / p.groups, first = (int)(part % p.groups) * len, units = len / 8;
-    const T *x = reinterpret_cast<const T *>(p.x) + row * p.x_stride + first;
-    const T *res = p.residual == nullptr ? nullptr
-                                         : reinterpret_cast<const T *>(p.residual) + row * p.dim + first;
-    float v[NU > 0 ? NU : 1][8];
-    float ss = 0.f;
-    if (NU > 0) {
+    const bool has_res = p.residual != nullptr, has_norm = p.weight != nullptr;
+    Raw8<T> x8[R], r8[R];
+    Raw8<float> w[R];
+    float v[R][8];
+    // The units u0, u0 + TPR, .. of a part: every load is unconditional (units
+    // behind the end read the last one), so that all of them are in flight together.
+    auto load = [&](int64_t at, int u0) {
+        const int64_t row = at / p.groups;
+        const T *x = reinterpret_cast<const T *>(p.x) + row * p.x_stride + first;
+        const T *res = reinterpret_cast<const T *>(p.residual) + row * p.dim + first;
 #pragma unroll
-        for (int i = 0; i < NU; ++i) {
-            const int u = tid + i * TPR;
-            if (u < units) {
-                load_unit(x, res, u, v[i]);
+        for (int i = 0; i < R; ++i)
+            x8[i].load(x + 8 * min(u0 + i * TPR, units - 1));
+        if (has_res) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                r8[i].load(res + 8 * min(u0 + i * TPR, units - 1));
+        }
+    };
+    auto load_w = [&](int u0) {
+        if (has_norm) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                w[i].load(p.weight + first + 8 * min(u0 + i * TPR, units - 1));
+        }
+    };
+    auto widen = [&]() {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[i][k] = has_res ? x8[i].get(k) + r8[i].get(k) : x8[i].get(k);
+    };
+    float ss;
+    auto square = [&](int u0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (u0 + i * TPR < units) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     ss = fmaf(v[i][k], v[i][k], ss);
             }
-        }
-    } else if (p.weight != nullptr) {
-        for (int u = tid; u < units; u += TPR) {
-            load_unit(x, res, u, v[0]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                ss = fmaf(v[0][k], v[0][k], ss);
-        }
-    }
-    float rs = 1.f;
-    if (p.weight != nullptr) {
-        ss = group_sum<32>(ss);
-        if (TPR > 32) {
-            if ((tid & 31) == 0)
-                red[tid >> 5] = ss;
-            __syncthreads();
-            ss = (tid & 31) < TPR / 32 ? red[tid & 31] : 0.f;
-            ss = group_sum<32>(ss);
-        }
-        rs = rsqrtf(ss / (float)len + p.eps);
-    }
+    };
     if (NU > 0) {
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-            if (TPR == 32 ? i * 32 < units : i * TPR + (tid & ~31) < units) // uniform over the warp
-                emit_unit<T>(p, tid + i * TPR < units, row, first, tid + i * TPR, rs, v[i]);
+        load(part, tid);
+        load_w(tid);
+    }
+    for (int turn = 0; part < parts; part += step, turn ^= 1) {
+        const int64_t row = part / p.groups;
+        ss = 0.f;
+        if (NU > 0) {
+            widen();
+            if (part + step < parts)
+                load(part + step, tid);
+            square(tid);
+        } else if (has_norm) {
+            for (int u = tid; u < units; u += TPR) {
+                load(part, u);
+                widen();
+                square(u);
+            }
         }
-    } else {
-        for (int u = tid; (u & ~31) < units; u += TPR) {
-            if (u < units)
-                load_unit(x, res, u, v[0]);
-            emit_unit<T>(p, u < units, row, first, u, rs, v[0]);
+        float rs = 1.f;
+        if (has_norm) {
+            ss = group_sum<32>(ss);
+            if (TPR > 32) { // the other turn's sums may still be read by slower warps
+                if ((tid & 31) == 0)
+                    red[turn][tid >> 5] = ss;
+                __syncthreads();
+                ss = (tid & 31) < TPR / 32 ? red[turn][tid & 31] : 0.f;
+                ss = group_sum<32>(ss);
+            }
+            rs = rsqrtf(ss / (float)len + p.eps);
+        }
+        if (NU > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if (TPR == 32 ? i * 32 < units : i * TPR + (tid & ~31) < units) // uniform over the warp
+                    emit_unit<T>(p, tid + i * TPR < units, row, first, tid + i * TPR, rs, w[i], v[i]);
+            }
+        } else {
+            for (int u = tid; (u & ~31) < units; u += TPR) {
+                load(part, u);
+                load_w(u);
+                widen();
+                emit_unit<T>(p, u < units, row, first, u, rs, w[0], v[0]);
+            }
         }
     }
 }
 
 template <typename T, int TPR, int NU> cudaError_t go(const NormArgs &p, cudaStream_t s) {
-    constexpr int kThreads = TPR < 256 ? 256 : TPR;
-    const int64_t parts = p.rows * p.groups;
-    norm_kernel<T, TPR, NU><<<(unsigned)((parts + kThreads / TPR - 1) / (kThreads / TPR)), kThreads, 0, s>>>(p);
+    constexpr int kThreads = TPR < 256 ? 256 : TPR, PER = kThreads / TPR;
+    const int64_t parts = p.rows * p.groups, all = (parts + PER - 1) / PER;
+    int64_t blocks = all;
+    // blocks that run at once: two to an SM, more where their registers are few
+    const int64_t at_once = (int64_t)148 * (NU == 1 ? 4 : 2);
+    if (NU > 0 && all > at_once && at_once >= p.groups)
+        blocks = at_once / p.groups * p.groups; // the step is a multiple of the groups
+    norm_kernel<T, TPR, NU><<<(unsigned)blocks, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -186,6 +226,9 @@ template <typename T> cudaError_t launch_t(const NormArgs &p, cudaStream_t s) {
         return go<T, 32, 1>(p, s);
     if (units <= 128)
         return go<T, 32, 4>(p, s);
+    // few rows: the row over more threads, for its latency
+    if (units > 256 && units <= 1024 && p.rows * p.groups <= 148)
+        return go<T, 1024, 1>(p, s);
     if (units <= 256)
         return go<T, 256, 1>(p, s);
     if (units <= 512)
