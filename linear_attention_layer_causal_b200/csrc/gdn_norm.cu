@@ -214,7 +214,7 @@ template <typename T, int TPR, int NU> cudaError_t go(const NormArgs &p, cudaStr
     int64_t blocks = all;
     // blocks that run at once: two to an SM, more where their registers are few
     const int64_t at_once = (int64_t)148 * (NU == 1 ? 4 : 2);
-    if (NU > 0 && all > at_once && at_once >= p.groups)
+    if (NU > 0 && all > 3 * at_once && at_once >= p.groups)
         blocks = at_once / p.groups * p.groups; // the step is a multiple of the groups
     norm_kernel<T, TPR, NU><<<(unsigned)blocks, kThreads, 0, s>>>(p);
     return cudaGetLastError();

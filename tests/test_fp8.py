@@ -52,6 +52,10 @@ def check_quant(q, scale, v, exact_scale):
     (6, 1024, 8, torch.bfloat16, True, 1.0),
     (3, 8192, 4, torch.float32, False, 0.0),
     (2, 40960, 2, torch.bfloat16, True, 0.0),
+    (2500, 2560, 1, torch.bfloat16, True, 1.0),   # a block takes several rows
+    (1100, 1536, 3, torch.bfloat16, False, 0.0),  # and several groups' parts
+    (8000, 136, 1, torch.float32, True, 1.0),
+    (1000, 8192, 1, torch.float32, True, 0.0),
 ])
 def test_norm(rows, dim, groups, dtype, residual, offset):
     x, w = (3 * randn(rows + dim, rows, dim)).to(dtype), 0.3 * randn(dim, dim)
