@@ -405,7 +405,9 @@ GDN_API gdn_status gdn_ssm_prefill_workspace_size(const gdn_ssm_config *cfg, int
  *   y             [N, H, P]         act_dtype
  *   final_state   [batch, H, P, S]  float32, or NULL; may equal initial_state
  *   final_conv    [batch, 3, H P + 2 G S] act_dtype, or NULL; may equal initial_conv
- * Rows at and behind cu_seqlens[batch] are left as they were.
+ * Rows at and behind cu_seqlens[batch] are left as they were.  A non-finite x,
+ * gate or state reaches the outputs that depend on it and no others.
+ * gdn_prefill_status reads the workspace's status words after the call.
  */
 GDN_API gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *params,
                                    const void *xbc, int64_t xbc_stride, const void *dt,
@@ -476,8 +478,9 @@ GDN_API gdn_status gdn_rmsnorm_fp8(const gdn_norm_config *cfg, const void *x, in
  * The products within a block are summed by the tensor core in float32, the
  * blocks in float32 registers.  K: a positive multiple of 16.  M, N and the
  * alignment of out's rows are free (out itself is 16-byte aligned, the scales
- * 4-byte).  Workspace: gdn_matmul_fp8_workspace_size bytes, 16-byte aligned
- * (0 for most shapes); calls that may overlap on the GPU need one each.
+ * 4-byte).  Workspace: gdn_matmul_fp8_workspace_size bytes, 16-byte aligned; it
+ * begins with status words that gdn_prefill_status reads after the call.  Calls
+ * that may overlap on the GPU need one each.
  */
 GDN_API gdn_status gdn_matmul_fp8_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
 GDN_API gdn_status gdn_matmul_fp8(const void *a, const float *a_scale, const void *w,

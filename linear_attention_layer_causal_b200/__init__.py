@@ -29,7 +29,7 @@ import ctypes
 import os
 from contextlib import nullcontext
 from dataclasses import dataclass
-from functools import cached_property
+from functools import cached_property, lru_cache
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -519,6 +519,10 @@ class SsmConfig:
                           self.conv_kernel, self.dt_min, self.dt_max,
                           GDN_BF16 if self.act_dtype == "bf16" else GDN_F32, self.segments)
 
+    @cached_property
+    def _workspace_sizes(self) -> dict:
+        return {}
+
     def _c(self) -> _SsmConfig:
         return self._struct
 
@@ -529,7 +533,7 @@ def _check(name, t, shape, dtype, device, optional=True):
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
     return t.data_ptr()
@@ -541,7 +545,7 @@ def _rows(name, t, shape, dtype, device, optional=False):
         if optional:
             return None, 0
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     strides, n = t.stride(), 1
@@ -585,11 +589,17 @@ def _workspace(workspace, need, device):
 
 
 def ssm_prefill_workspace_size(cfg: SsmConfig, batch: int, total_tokens: int) -> int:
+    """Bytes of workspace (gdn_ssm_prefill_workspace_size), asked once for each size."""
+    known = cfg._workspace_sizes.get((batch, total_tokens))
+    if known is not None:
+        return known
     n = ctypes.c_size_t(0)
     st = lib().gdn_ssm_prefill_workspace_size(ctypes.byref(cfg._c()), batch, total_tokens,
                                               ctypes.byref(n))
     if st != GDN_OK:
         raise GdnError(st, "gdn_ssm_prefill_workspace_size")
+    if len(cfg._workspace_sizes) < 4096:
+        cfg._workspace_sizes[batch, total_tokens] = n.value
     return n.value
 
 
@@ -610,7 +620,8 @@ def ssm_prefill(cfg: SsmConfig, xbc, dt, cu_seqlens, conv_w, A_log, *, conv_b=No
 
     xbc [N, H P + 2 G S], dt [N, H] and z [N, H, P] may be slices of wider rows.  Returns a dict
     with "y" [N, H, P] and, when requested or passed in, "final_state" [B, H, P, S] float32 and
-    "final_conv" [B, 3, H P + 2 G S]; ``final_state`` may be ``initial_state``."""
+    "final_conv" [B, 3, H P + 2 G S]; ``final_state`` may be ``initial_state``, and ``final_conv``
+    ``initial_conv``."""
     import torch
     N, B, dev, act = xbc.shape[0], cu_seqlens.shape[0] - 1, xbc.device, _act(cfg)
     H, P, S, C = cfg.num_heads, cfg.head_dim, cfg.state_dim, cfg.conv_dim
@@ -674,6 +685,11 @@ def ssm_decode(cfg: SsmConfig, xbc, dt, state, conv_cache, conv_w, A_log, *, con
 BLOCK = 128  # elements that share a scale
 
 
+@lru_cache(maxsize=1024)
+def _norm_config(*fields) -> _NormConfig:
+    return _NormConfig(*fields)
+
+
 def _norm_call(x, weight, residual, groups, eps, weight_offset, q, scale, residual_out, y, want_r,
                want_y, stream):
     import torch
@@ -693,7 +709,7 @@ def _norm_call(x, weight, residual, groups, eps, weight_offset, q, scale, residu
             residual_out = torch.empty(shape, dtype=act, device=dev)
         if y is None and want_y:
             y = torch.empty(shape, dtype=act, device=dev)
-        cfg = _NormConfig(rows, dim, groups, eps, weight_offset, GDN_BF16 if act == torch.bfloat16 else GDN_F32)
+        cfg = _norm_config(rows, dim, groups, eps, weight_offset, GDN_BF16 if act == torch.bfloat16 else GDN_F32)
         st = lib().gdn_rmsnorm_fp8(
             ctypes.byref(cfg), xp, xs, _check("residual", residual, shape, act, dev),
             _check("weight", weight, (dim,), torch.float32, dev),
@@ -728,6 +744,7 @@ def quantize_fp8(x, *, q=None, scale=None, stream=None):
     return _norm_call(x, None, None, 1, 0.0, 0.0, q, scale, None, None, False, False, stream)[:2]
 
 
+@lru_cache(maxsize=1024)
 def matmul_fp8_workspace_size(M: int, N: int, K: int) -> int:
     n = ctypes.c_size_t(0)
     st = lib().gdn_matmul_fp8_workspace_size(M, N, K, ctypes.byref(n))

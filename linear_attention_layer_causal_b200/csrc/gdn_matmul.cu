@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (blockIdx.x == 0)
-            *status = 0;
+            status[0] = status[1] = 0;
     }
     if (warp == 1)
         tmem_alloc(smem_u32(&tmem_base), 2 * BN);
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (blockIdx.x == 0)
-            *status = 0;
+            status[0] = status[1] = 0;
     }
     if (warp == 1)
         tmem_alloc(smem_u32(&tmem_base), T::kTmem);

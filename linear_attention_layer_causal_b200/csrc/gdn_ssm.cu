@@ -13,8 +13,16 @@
 // ssm_scan_kernel, per sequence (or segment of it) and 128 state rows (two
 // heads of 64 or one of 128): the three products above as tcgen05 MMAs of 128
 // rows, with x^T, x'^T and H as the operand in TMEM and C, B and M in shared
-// memory, and the rest in warpgroups of their own: convolving x (X), the decay
-// masks M (M), the state in registers (S, two of them), the output (Y).
+// memory; two warps make the masks M, and 16 convolve x, keep the state in
+// registers and gate and store the output.
+// With few sequences each is cut into segments, and a first run of the scan
+// kernel, without outputs, finds what each segment adds to the state.
+//
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 227 us (prep
+// 28, summary 44, output pass 150 to 160), where moving the bytes would take 35
+// and the MMAs 50.  What bounds it is the 16 warps' instructions: about 9000
+// cycles a chunk (two splits, two SiLUs and an exponential for each value), of
+// which the tensor core is busy 2300.
 //
 // Precision: every operand of a product is the sum of two bfloat16 parts, each
 // product three MMAs (the product of the two second parts is left out): about
@@ -124,6 +132,20 @@ template <typename T> __device__ __forceinline__ const T *conv_row(const SsmArgs
     return reinterpret_cast<const T *>(p.init_conv) + ((int64_t)n * 3 + 3 + (t - start)) * p.conv_dim();
 }
 
+// Channel c of the window after sequence n: the last three rows of [initial
+// window; sequence].  Read before written: the windows may be the same.
+template <typename T> __device__ __forceinline__ void final_window(const SsmArgs &p, int n, int64_t start, int64_t end, int c) {
+    T v[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const T *row = conv_row<T>(p, n, start, end - 3 + i);
+        v[i] = row != nullptr ? row[c] : from_f<T>(0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        reinterpret_cast<T *>(p.final_conv)[((int64_t)n * 3 + i) * p.conv_dim() + c] = v[i];
+}
+
 // ------------------------------------------------------------------- prep
 
 constexpr int kPrepThreads = 512;
@@ -154,7 +176,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
     const int64_t id = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (id == 0 && g == 0 && blockIdx.z == 0 && tid == 0)
-        *status = 0;
+        status[0] = status[1] = 0;
     // the sequence of this chunk number: the last n with first_chunk(cu[n]) <= id
     int lo = 0, hi = p.batch - 1;
     while (lo < hi) {
@@ -495,7 +517,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     };
     auto gate_ready = [&](int c, bool patient = false) { return wait_all(kGFull + c % K::kGateSlots, (c / K::kGateSlots) & 1, patient); };
     auto i_done = [&](int c, bool patient = false) { return wait_all(kIDone + (c & 1), (c >> 1) & 1, patient); };
-    const int row = 32 * q + lane;          // state row of a thread of the X, S, Y warpgroups
+    const int row = 32 * q + lane;          // a worker thread's state row
     const int hl = P == 64 ? q >> 1 : 0;    // its head within the block (uniform over the warp)
     const bool live = hl < u.nh;
     const int64_t chan = (int64_t)u.h0 * P + row; // its x channel
@@ -572,7 +594,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         break;
                     tc_fence_after();
                     // Y: D[row][t] = sum_s H[row][s] C[t][s].  H hi of 16 columns kk sits beside lo in the
-                    // quarter of DH that its S warpgroup owns.
+                    // quarter of DH that its warpgroup owns.
                     const uint32_t ch = base + slot * K::kHalf, cl = ch + S * 128, yi = tmem + (ph ? K::kYI2 : K::kYI);
 #pragma unroll
                     for (int kk = 0; kk < S / 16; ++kk) {
@@ -979,24 +1001,24 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         tmem_relinquish();
         tmem_dealloc(tmem, kTmemCols);
     }
+    // The window after the sequence, by the blocks that have its first chunk (a short sequence's first segments may
+    // have none): they alone read the initial window of their x channels, and have; B's and C's was read by the
+    // kernel before this one.
+    if (!SUMMARY && p.final_conv != nullptr && (u.nc > 0 ? u.c0 == 0 : u.seg == 0 && u.start == u.end)) {
+        for (int i = tid; i < u.nh * P; i += kScanThreads)
+            final_window<T>(p, u.n, u.start, u.end, u.h0 * P + i);
+        if (u.tile % a.tiles_per_group == 0) {
+            for (int i = tid; i < 2 * S; i += kScanThreads)
+                final_window<T>(p, u.n, u.start, u.end, p.H * P + (i < S ? u.g * S + i : p.G * S + u.g * S + i - S));
+        }
+    }
 }
 
-// The last three pre-conv rows of [initial window; sequence].
+// The windows of a call without tokens.
 template <typename T> __global__ void __launch_bounds__(256) ssm_final_conv_kernel(const SsmArgs p) {
-    const int C = p.conv_dim(), c = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
-    if (c >= C)
-        return;
-    int64_t s, e;
-    seq_bounds(p.cu, n, p.N, s, e);
-    T v[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const T *row = conv_row<T>(p, n, s, e - 3 + i);
-        v[i] = row != nullptr ? row[c] : from_f<T>(0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-        reinterpret_cast<T *>(p.final_conv)[((int64_t)n * 3 + i) * C + c] = v[i];
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c < p.conv_dim())
+        final_window<T>(p, blockIdx.y, 0, 0, c);
 }
 
 // The cut of the sequences: segments of the output pass, and how many parts the
@@ -1064,7 +1086,10 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
         e = cudaGetLastError();
         if (e == cudaSuccess)
             e = record_if(end, s);
-    } else if (p.final_state != nullptr && p.final_state != p.init_state) { // no tokens: the states pass through
+        return e;
+    }
+    // no tokens: the states and windows pass through
+    if (p.final_state != nullptr && p.final_state != p.init_state) {
         const size_t bytes = (size_t)p.batch * p.H * P * S * 4;
         e = p.init_state != nullptr ? cudaMemcpyAsync(p.final_state, p.init_state, bytes, cudaMemcpyDeviceToDevice, s)
                                     : cudaMemsetAsync(p.final_state, 0, bytes, s);

@@ -381,3 +381,150 @@ def test_binding_refuses_wrong_shapes_types_and_strides():
         prefill(cfg, {**d, "xbc": odd}, cu)
     with pytest.raises(gdn.GdnError):
         prefill(cfg, d, cu, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("segments", [1, 4, 16])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_in_place_with_segments_and_short_sequences(segments, dtype):
+    """States and windows advance in place, whichever segment has a short sequence's only chunk."""
+    lens = [1, 64, 2, 130, 0, 3, 65, 700] + 24 * [1, 5]
+    cfg = gdn.SsmConfig(2, 6, 64, 64, act_dtype=dtype, segments=segments)
+    d, cu = make(cfg, lens, 40 + segments)
+    e = want(cfg, d, lens)
+    S0, C0 = d["initial_state"].clone(), d["initial_conv"].clone()
+    out = prefill(cfg, {**d, "initial_state": S0, "initial_conv": C0}, cu, final_state=S0, final_conv=C0)
+    near(out["y"], e["y"], e["y_mag"], "y")
+    near(S0, e["state"], e["state_mag"], "state")
+    assert torch.equal(C0, e["conv"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [0, 37, 63, 64, 100])
+def test_a_non_finite_channel_of_x_stays_in_its_row(at, value):
+    """x of one channel and token is not finite: that channel's outputs from there on, and no others."""
+    cfg = gdn.SsmConfig(1, 2, 64, 64, act_dtype="f32")
+    d, cu = make(cfg, [150], 15, gate=False)
+    clean = prefill(cfg, d, cu, return_final_state=True)
+    xbc = d["xbc"].clone()
+    xbc[at, 70] = value  # head 1, channel 6
+    out = prefill(cfg, {**d, "xbc": xbc}, cu, return_final_state=True)
+    others = [c for c in range(128) if c != 70]
+    y, y0 = out["y"].flatten(1), clean["y"].flatten(1)
+    assert torch.equal(y[:, others], y0[:, others])
+    assert torch.equal(y[:at, 70], y0[:at, 70])
+    assert not y[at:, 70].isfinite().any()
+    S, S0 = out["final_state"].flatten(1, 2)[0], clean["final_state"].flatten(1, 2)[0]
+    assert torch.equal(S[others], S0[others]) and not S[70].isfinite().any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", ["B", "C"])
+def test_a_non_finite_column_of_b_or_c(which):
+    """From a bad B on every output of its group; a bad C is read by four tokens and the state has no part of it."""
+    cfg = gdn.SsmConfig(2, 4, 64, 64, act_dtype="f32")
+    d, cu = make(cfg, [150], 17, gate=False)
+    clean = prefill(cfg, d, cu, return_final_state=True)
+    xbc, at = d["xbc"].clone(), 40
+    xbc[at, 4 * 64 + (2 * 64 if which == "C" else 0) + 64 + 5] = float("nan")  # group 1, column 5
+    out = prefill(cfg, {**d, "xbc": xbc}, cu, return_final_state=True)
+    y, y0 = out["y"], clean["y"]
+    end = at + 4 if which == "C" else 150
+    assert torch.equal(y[:, :2], y0[:, :2])
+    assert torch.equal(y[:at], y0[:at]) and torch.equal(y[end:], y0[end:])
+    assert y[at:end, 2:].isnan().all()
+    S, S0 = out["final_state"][0], clean["final_state"][0]
+    if which == "C":
+        assert torch.equal(S, S0)
+    else:
+        cols = [c for c in range(64) if c != 5]
+        assert torch.equal(S[:2], S0[:2]) and torch.equal(S[2:, :, cols], S0[2:, :, cols])
+        assert S[2:, :, 5].isnan().all()
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once_without_given_workspaces():
+    """Calls that overlap, each with a workspace of its own that is freed at once."""
+    cfg = gdn.SsmConfig(1, 4, 64, 128, segments=4)
+    lens = [900, 300]
+    d, cu = make(cfg, lens, 18)
+    d2, _ = make(cfg, lens, 19)
+    one = prefill(cfg, d, cu, return_final_state=True)
+    two = prefill(cfg, d2, cu, return_final_state=True)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(6):
+        got.append((prefill(cfg, d, cu, return_final_state=True, stream=sa), one))
+        got.append((prefill(cfg, d2, cu, return_final_state=True, stream=sb), two))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a["y"], b["y"]) and torch.equal(a["final_state"], b["final_state"])
+
+
+@pytest.mark.gpu
+def test_cu_seqlens_that_end_early_or_are_out_of_order():
+    """Only the rows that some sequence has are written, and nothing outside the tensors is read."""
+    cfg = gdn.SsmConfig(1, 2, 64, 64, act_dtype="f32")
+    d, cu = make(cfg, [100, 50], 20)
+    y = torch.full((150, 2, 64), 7.0, device="cuda")
+    clean = prefill(cfg, d, cu)["y"]
+    cu2 = torch.tensor([0, 100, 100], dtype=torch.int32, device="cuda")
+    prefill(cfg, d, cu2, y=y)
+    assert torch.equal(y[:100], clean[:100]) and (y[100:] == 7.0).all()
+    y.fill_(7.0)
+    cu2 = torch.tensor([0, 100, 1000], dtype=torch.int32, device="cuda")  # past the rows: the last one ends it
+    prefill(cfg, d, cu2, y=y)
+    assert torch.equal(y, clean)
+    y.fill_(7.0)
+    cu2 = torch.tensor([0, 100, 20], dtype=torch.int32, device="cuda")  # a negative length is none
+    prefill(cfg, d, cu2, y=y)
+    assert torch.equal(y[:100], clean[:100]) and (y[100:] == 7.0).all()
+
+
+@pytest.mark.gpu
+def test_status_words_are_clear_after_a_call():
+    cfg = gdn.SsmConfig(1, 2, 64, 64)
+    d, cu = make(cfg, [100], 21)
+    need = gdn.ssm_prefill_workspace_size(cfg, 1, 100)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    prefill(cfg, d, cu, workspace=ws)
+    torch.cuda.synchronize()
+    assert (ws[:8] == 0).all()
+
+
+@pytest.mark.gpu
+def test_prefill_and_decode_past_32_bit_offsets():
+    """Rows, outputs and states whose offsets pass 2^31 elements give what the same rows give alone."""
+    cfg = gdn.SsmConfig(1, 128, 64, 64, segments=1)
+    N, C = 262200, cfg.conv_dim
+    total = N + 70
+    assert total * 64 * 128 > 2 ** 31
+    xbc = torch.zeros(total, C, dtype=torch.bfloat16, device="cuda")
+    d, _ = make(cfg, [70], 23, init=False, gate=False)
+    dt = torch.zeros(total, 128, dtype=torch.bfloat16, device="cuda")
+    xbc[-70:], dt[-70:] = d["xbc"], d["dt"]
+    cu = torch.tensor([0, N, total], dtype=torch.int32, device="cuda")
+    out = prefill(cfg, {**d, "xbc": xbc, "dt": dt}, cu, return_final_state=True)
+    alone = prefill(cfg, d, torch.tensor([0, 70], dtype=torch.int32, device="cuda"), return_final_state=True)
+    assert torch.equal(out["y"][-70:], alone["y"])
+    assert torch.equal(out["final_state"][1], alone["final_state"][0])
+    del xbc, dt, out
+    torch.cuda.empty_cache()
+
+    B = 4200
+    assert B * 128 * 64 * 64 > 2 ** 31
+    state = torch.zeros(B, 128, 64, 64, device="cuda")
+    state[-1] = alone["final_state"][0]
+    conv = torch.zeros(B, 3, C, dtype=torch.bfloat16, device="cuda")
+    xb = torch.zeros(B, C, dtype=torch.bfloat16, device="cuda")
+    dt1 = torch.zeros(B, 128, dtype=torch.bfloat16, device="cuda")
+    xb[-1], dt1[-1] = d["xbc"][0], d["dt"][0]
+    kw = {k: d[k] for k in ("conv_b", "dt_bias", "D")}
+    S1, C1 = state[-1:].clone(), conv[-1:].clone()
+    y = gdn.ssm_decode(cfg, xb, dt1, state, conv, d["conv_w"], d["A_log"], **kw)
+    y1 = gdn.ssm_decode(cfg, xb[-1:], dt1[-1:], S1, C1, d["conv_w"], d["A_log"], **kw)
+    assert torch.equal(conv[-1:], C1)
+    for a, b in ((state[-1], S1[0]), (y[-1].float(), y1[0].float())):
+        assert float((a - b).norm()) <= 2.0 ** -8 * float(b.norm())
