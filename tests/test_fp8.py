@@ -309,3 +309,41 @@ def test_binding_refuses_wrong_shapes_types_and_strides():
             gdn.matmul_fp8(*bad)
     with pytest.raises(ValueError):
         gdn.matmul_fp8(a, sa, b, sb, out=torch.empty(4, 9, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_past_32_bit_offsets():
+    """Rows whose offsets pass 2^31 elements give what they give alone."""
+    rows, dim = 300000, 8192
+    assert rows * dim > 2 ** 31
+    x = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = randn(60, 3, dim).bfloat16()
+    w = randn(61, dim)
+    out, alone = gdn.rmsnorm_fp8(x, w), gdn.rmsnorm_fp8(x[-3:], w)
+    assert torch.equal(out["q"][-3:].view(torch.uint8), alone["q"].view(torch.uint8))
+    assert torch.equal(out["scale"][-3:], alone["scale"])
+    del x
+    a, sa, wq, sw = operands(300, 12352, 128, 62)
+    M = 180000
+    assert M * 12352 > 2 ** 31
+    big = torch.zeros(M, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.zeros(M, 1, device="cuda")
+    big.view(torch.uint8)[-300:] = a.view(torch.uint8)
+    scales[-300:] = sa
+    assert torch.equal(gdn.matmul_fp8(big, scales, wq, sw)[-300:], gdn.matmul_fp8(a, sa, wq, sw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 300])
+def test_two_streams_and_status_words(M):
+    """Products that overlap, with workspaces of their own; a given one comes back with clear status words."""
+    a, sa, w, sw = operands(M, 1000, 2048, 63)
+    want = gdn.matmul_fp8(a, sa, w, sw)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [gdn.matmul_fp8(a, sa, w, sw, stream=s) for _ in range(6) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    ws = torch.full((gdn.matmul_fp8_workspace_size(M, 1000, 2048),), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(gdn.matmul_fp8(a, sa, w, sw, workspace=ws), want)
+    assert (ws[:8] == 0).all()
