@@ -18,11 +18,11 @@
 // With few sequences each is cut into segments, and a first run of the scan
 // kernel, without outputs, finds what each segment adds to the state.
 //
-// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 227 us (prep
-// 28, summary 44, output pass 150 to 160), where moving the bytes would take 35
-// and the MMAs 50.  What bounds it is the 16 warps' instructions: about 9000
-// cycles a chunk (two splits, two SiLUs and an exponential for each value), of
-// which the tensor core is busy 2300.
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 206 us (prep
+// 28, summary 41, output pass 148), where moving the bytes would take 35 and
+// the MMAs 50.  What bounds it is the 16 warps' instructions: about 8000 cycles
+// a chunk (21000 instructions on 4 schedulers: the splits, the convolution, two
+// SiLUs), of which the tensor core is busy 2300.
 //
 // Precision: every operand of a product is the sum of two bfloat16 parts, each
 // product three MMAs (the product of the two second parts is left out): about
@@ -39,7 +39,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kQ = 64;        // tokens of a chunk
-constexpr int kGateRec = 320; // floats of a (chunk, head): G / ln 2, its low part, -ln 2 delta, -ln 2 x' weight, e^G
+constexpr int kMaskRec = 192; // floats of a (chunk, head) for M: G / ln 2, its low part, -ln 2 delta
+constexpr int kGateRec = 128; // and for the rest: -ln 2 x' weight, e^G
 constexpr int kSMs = 148;
 constexpr uint32_t kStatusTimeout = 1u;
 
@@ -52,7 +53,7 @@ __device__ __forceinline__ int64_t first_chunk(int64_t start, int n) { return st
 int64_t max_chunks(int64_t N, int batch) { return N / kQ + batch; }
 
 struct Layout { // workspace offsets in bytes
-    size_t bc, cb, gates, seg, segdecay, total;
+    size_t bc, cb, masks, gates, seg, segdecay, total;
 };
 Layout layout(int G, int H, int P, int S, int64_t N, int batch, int slots) {
     const size_t chunks = (size_t)max_chunks(N, batch);
@@ -60,7 +61,8 @@ Layout layout(int G, int H, int P, int S, int64_t N, int batch, int slots) {
     Layout l;
     l.bc = kWorkspaceHeader;
     l.cb = l.bc + round_up(chunks * G * kQ * 4 * S * 2);
-    l.gates = l.cb + round_up(chunks * G * kQ * kQ * 4);
+    l.masks = l.cb + round_up(chunks * G * kQ * kQ * 4);
+    l.gates = l.masks + round_up(chunks * H * kMaskRec * 4);
     l.seg = l.gates + round_up(chunks * H * kGateRec * 4);
     l.segdecay = l.seg + (slots > 1 ? round_up((size_t)batch * tiles * slots * 128 * S * 4) : 0);
     l.total = l.segdecay + (slots > 1 ? round_up((size_t)batch * tiles * slots * 2 * 4) : 0);
@@ -83,6 +85,16 @@ __device__ __forceinline__ float2 unpack(f2 v) {
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     f2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 // Two floats as bfloat16 parts: hi = the nearest, lo = what is left, each
@@ -117,8 +129,13 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// SiLU(x) = x / (1 + 2^p), p = -x log2(e).
+// SiLU(x) = x / (1 + 2^p), p = -x log2(e); also times y, for a pair.
 __device__ __forceinline__ float silu(float x) { return x * rcp(1.f + ex2(-kLog2e * x)); }
+__device__ __forceinline__ float2 gated(f2 y, f2 x) {
+    const float2 e = unpack(mul2(x, pack(-kLog2e, -kLog2e)));
+    const float2 d = unpack(add2(pack(ex2(e.x), ex2(e.y)), pack(1.f, 1.f)));
+    return unpack(mul2(mul2(x, pack(rcp(d.x), rcp(d.y))), y));
+}
 // SiLU(x) / -ln 2 = p / (1 + 2^p).
 __device__ __forceinline__ float silu_scaled(float p) { return p * rcp(1.f + ex2(p)); }
 
@@ -166,10 +183,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 // One chunk and group; the blocks of z = 1 have the gates.  Writes, for the scan kernel: the rows [64][4 S] of
 // B hi | B lo | C hi | C lo (zero behind the sequence's end), the 64 x 64
-// products C_t . B_s of s's and t's 16-blocks with s <= t, and a gate record
-// for each head of the group.
+// products C_t . B_s of s's and t's 16-blocks with s <= t, and the records of
+// each head of the group.
 template <typename T, int S>
-__global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs p, __nv_bfloat16 *bc, float *cb, float *gates,
+__global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs p, __nv_bfloat16 *bc, float *cb, float *masks, float *gates,
                                                                 uint32_t *status) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int LDS = S + 8; // row length in shared memory: rows 16 bytes apart in banks
@@ -229,18 +246,18 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
             if (lane == 0)
                 before = 0.0;
             const double all = __shfl_sync(0xffffffffu, sum, 31);
-            float *rec = gates + (id * p.H + h) * kGateRec + 2 * lane;
+            float *mask = masks + (id * p.H + h) * kMaskRec + 2 * lane, *rec = gates + (id * p.H + h) * kGateRec + 2 * lane;
     #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const double G = before + s[i];
                 const double G2 = G * 1.4426950408889634; // for base-2 exponentials
                 const float gh = (float)G2;
-                rec[i] = gh;
-                rec[64 + i] = (float)(G2 - (double)gh);
+                mask[i] = gh;
+                mask[64 + i] = (float)(G2 - (double)gh);
                 // times -ln 2: the scan kernel's x is SiLU(x) / -ln 2
-                rec[128 + i] = -kLn2 * d[i];
-                rec[192 + i] = d[i] == 0.f ? 0.f : -kLn2 * (d[i] * expf((float)(all - G)));
-                rec[256 + i] = expf((float)G);
+                mask[128 + i] = -kLn2 * d[i];
+                rec[i] = d[i] == 0.f ? 0.f : -kLn2 * (d[i] * expf((float)(all - G)));
+                rec[64 + i] = expf((float)G);
             }
         }
         return;
@@ -365,15 +382,16 @@ template <typename T, int P, int S> struct Scan {
     static constexpr int kCW = S / 4;                 // state columns of a worker warpgroup
     static constexpr int kHalf = 2 * S * kQ * 2;      // bytes of a chunk's B (or C): hi, lo
     static constexpr int kSlots = 3;                  // of them in shared memory: C, B, C, B, ... in turn
-    static constexpr int kGateSlots = 4;
+    static constexpr int kGateSlots = 4;              // of the chunks' weights: in use by two, on their way for two
     static constexpr int kMBytes = kHeads * 2 * kQ * kQ * 2; // M hi of the heads, then lo
     static constexpr int kMBufs = sizeof(T) == 2 ? 2 : 1;
-    static constexpr int kCbBytes = kQ * kQ * 4;
+    static constexpr int kCbBufs = kMBufs;
+    static constexpr int kCbBytes = 3 * 32 * 32 * 4;  // C B^T without its upper right quarter
     static constexpr int kRow = 128 * sizeof(T);      // 128 channels of a token
-    static constexpr int kXBytes = (kQ + 3) * kRow;   // x; and z, or the next x
-    static constexpr int kOffM = kSlots * kHalf, kOffCb = kOffM + kMBufs * kMBytes, kOffX = kOffCb + kCbBytes,
+    static constexpr int kXBytes = (kQ + 3) * kRow;   // x; the summary pass has its second buffer where M is
+    static constexpr int kOffM = kSlots * kHalf, kOffCb = kOffM + kMBufs * kMBytes, kOffX = kOffCb + kCbBufs * kCbBytes,
                          kOffZ = kOffX + kXBytes;
-    static constexpr size_t kSmem = 1024 + kOffZ + kXBytes;
+    static constexpr size_t kSmem = 1024 + kOffZ + kQ * kRow;
     // TMEM columns
     static constexpr uint32_t kDH = 0;             // x' B^T, then H hi and lo of the next chunk
     static constexpr uint32_t kYI = 128;           // H C^T
@@ -382,13 +400,12 @@ template <typename T, int P, int S> struct Scan {
     static constexpr uint32_t kX = 384;            // x hi, lo
     static constexpr uint32_t kYI2 = 448;          // the other buffer of H C^T
 };
-constexpr int kScanThreads = 640, kWorkers = 512;
+constexpr int kScanThreads = 640;
 constexpr uint32_t kTmemCols = 512;
 
-// B and C slots, M buffers, gate slots, and single barriers
+// B and C slots, M buffers, buffers of C B^T and of raw x, and single barriers
 enum Bar {
-    kBcFull = 0, kBcEmpty = 3, kMFull = 6, kIDone = 8, kGFull = 10, kGEmpty = 14,
-    kHFull = 18, kXFull, kUDone, kCbFull, kCbEmpty, kDrain, kBars
+    kBcFull = 0, kBcEmpty = 3, kMFull = 6, kIDone = 8, kCbFull = 10, kCbEmpty = 12, kRawFull = 14, kRawEmpty = 16, kHFull = 18, kXFull, kUDone, kDrain, kZFull, kZEmpty, kBars
 };
 
 // What a block works on.
@@ -418,34 +435,32 @@ __device__ __forceinline__ Unit unit_of(const SsmArgs &p, int segments, int tile
 
 struct ScanArgs {
     SsmArgs p;
-    const float *cb, *gates;
+    const float *cb, *masks, *gates;
     float *seg, *segdecay;
     uint32_t *status;
     int segments, fine, tiles_per_group; // the summary pass cuts every segment into `fine`
 };
 
-// The `n` threads of some warpgroups (named barrier `id`).
-__device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-
 // Warpgroup 0: a warp that loads, a warp that issues the MMAs, two that make M.
-// The other four work in step, each on 16 tokens of a chunk and a quarter of
-// the state's columns: while the tensor core has Y and U of chunk c, they gate
+// The other four take the same steps, each on 16 tokens of a chunk and a quarter
+// of the state's columns: while the tensor core has Y and U of chunk c, they gate
 // and store the output of chunk c - 1 and convolve x of chunk c + 1.  With a
 // role per warpgroup instead (x, state, output) every role was one or two warps
-// of a scheduler, too few to hide their own latencies: 8500 cycles a chunk.
+// of a scheduler, too few to hide their own latencies.  They meet only through
+// the mbarriers of what they share, so that a warp in its exponentials runs
+// beside one in its splits (with two meetings of all 16 a chunk: 227 us for the
+// 206 above, with copies of x and z by their own threads).
 // SUMMARY: only the states of the segments but the last, from zero (the first
 // from the initial state, which is also copied); no output.
 template <typename T, int P, int S, bool SUMMARY>
 __global__ void __launch_bounds__(kScanThreads, 1)
-    ssm_scan_kernel(const __grid_constant__ CUtensorMap tbc, const __grid_constant__ CUtensorMap tcb, const ScanArgs a) {
+    ssm_scan_kernel(const __grid_constant__ CUtensorMap tbc, const __grid_constant__ CUtensorMap tcb,
+                    const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tz, const ScanArgs a) {
     using K = Scan<T, P, S>;
     constexpr int NH = K::kHeads, CW = K::kCW;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
-    __shared__ __align__(16) float gate[K::kGateSlots][NH][kGateRec];
+    __shared__ __align__(16) float gate[K::kGateSlots][NH][kGateRec], mask[K::kCbBufs][NH][kMaskRec];
     __shared__ __align__(4) uint8_t bad[2][128][4]; // per row and 16 tokens: the first with a non-finite x, or kQ
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -467,16 +482,18 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             mbar_init(bar(kMFull + i), 2);
             mbar_init(bar(kIDone + i), 1);
         }
-        for (int i = 0; i < K::kGateSlots; ++i) {
-            mbar_init(bar(kGFull + i), 1);
-            mbar_init(bar(kGEmpty + i), SUMMARY ? 16 : 18); // the workers' warps, and M's
-        }
         mbar_init(bar(kXFull), 16);
         mbar_init(bar(kHFull), 16);
         mbar_init(bar(kUDone), 1);
-        mbar_init(bar(kCbFull), 1);
-        mbar_init(bar(kCbEmpty), 2);
         mbar_init(bar(kDrain), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kCbFull + i), 1);
+            mbar_init(bar(kCbEmpty + i), 2);
+            mbar_init(bar(kRawFull + i), 1);
+            mbar_init(bar(kRawEmpty + i), 16);
+        }
+        mbar_init(bar(kZFull), 1);
+        mbar_init(bar(kZEmpty), 16);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -515,8 +532,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         if (lane == 0)
             mbar_arrive(bar(i));
     };
-    auto gate_ready = [&](int c, bool patient = false) { return wait_all(kGFull + c % K::kGateSlots, (c / K::kGateSlots) & 1, patient); };
     auto i_done = [&](int c, bool patient = false) { return wait_all(kIDone + (c & 1), (c >> 1) & 1, patient); };
+    const int64_t tok0 = u.start + u.c0 * kQ;
+    // raw x: the summary pass has no M, whose room is its second buffer
+    auto raw_slot = [](int c) { return SUMMARY ? c & 1 : 0; };
+    auto raw_phase = [](int c) { return (uint32_t)(SUMMARY ? c >> 1 : c) & 1; };
     const int row = 32 * q + lane;          // a worker thread's state row
     const int hl = P == 64 ? q >> 1 : 0;    // its head within the block (uniform over the warp)
     const bool live = hl < u.nh;
@@ -526,46 +546,71 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0) {
             if (lane == 0) { // ---- loads
-                const int gbytes = u.nh * kGateRec * 4;
+                const int gbytes = u.nh * kGateRec * 4, mbytes = u.nh * kMaskRec * 4;
                 // slots of B and C in the order of their use: C B C B ..., or B B ... in the summary
                 int slot = 0, used = 0;
                 uint32_t ph = 1;
-                bool ok = true;
-                for (int c = 0; ok && c < u.nc; ++c) {
-                    const int gs = c % K::kGateSlots;
-                    if (!(ok = wait(kGEmpty + gs, ((c / K::kGateSlots) & 1) ^ 1, true)))
-                        break;
-                    mbar_arrive_expect_tx(bar(kGFull + gs), gbytes);
-                    bulk_load(smem_u32(gate[gs]), a.gates + ((id0 + c) * p.H + u.h0) * kGateRec, gbytes, bar(kGFull + gs));
-                    const int y = (int)(((id0 + c) * p.G + u.g) * kQ);
-                    if (!SUMMARY) {
-                        if (!(ok = wait(kCbEmpty, (c & 1) ^ 1, true))) {
-                            mbar_wait_bounded(bar(kGFull + gs), (c / K::kGateSlots) & 1, kDefaultWaitLimit);
-                            break;
-                        }
-                        mbar_arrive_expect_tx(bar(kCbFull), K::kCbBytes);
-                        tma_load_2d(base + K::kOffCb, &tcb, 0, y, bar(kCbFull));
-                        tma_load_2d(base + K::kOffCb + 8192, &tcb, 32, y, bar(kCbFull));
+                auto load_bc = [&](int y, int from) {
+                    if (!wait(kBcEmpty + slot, ph, true))
+                        return false;
+                    mbar_arrive_expect_tx(bar(kBcFull + slot), K::kHalf);
+                    for (int k = 0; k < 2 * S / 64; ++k) // boxes of 64 channels: hi, lo
+                        tma_load_2d(base + slot * K::kHalf + k * 8192, &tbc, 64 * k + from, y, bar(kBcFull + slot));
+                    used = used < K::kSlots ? used + 1 : K::kSlots;
+                    if (++slot == K::kSlots) {
+                        slot = 0;
+                        ph ^= 1;
                     }
-                    for (int part = SUMMARY ? 1 : 0; part < 2; ++part) { // C (channels 2 S ..), then B
-                        if (!(ok = wait(kBcEmpty + slot, ph, true))) {
-                            mbar_wait_bounded(bar(kGFull + gs), (c / K::kGateSlots) & 1, kDefaultWaitLimit);
-                            if (!SUMMARY)
-                                mbar_wait_bounded(bar(kCbFull), c & 1, kDefaultWaitLimit);
+                    return true;
+                };
+                // In the order in which the room for them comes free: that of z of chunk c - 2 does before that of
+                // x of chunk c, and both before C B^T's and B's.  Rows of x before the sequence or behind it, and of z behind it, are another
+                // sequence's, or zeros; channels of absent heads are whatever lies there.  Neither is used.
+                int cbs = 0, raws = 0, zs = 0; // loaded so far
+                bool ok = true;
+                for (int c = 0; ok && c < (SUMMARY ? u.nc : u.nc + 2); ++c) {
+                    const int y = (int)(((id0 + c) * p.G + u.g) * kQ);
+                    if (!SUMMARY && c < u.nc && !(ok = load_bc(y, 2 * S))) // C
+                        break;
+                    if (!SUMMARY && c >= 2 && p.z != nullptr) {
+                        if (!(ok = wait(kZEmpty, (c & 1) ^ 1)))
                             break;
+                        mbar_arrive_expect_tx(bar(kZFull), kQ * K::kRow);
+                        tma_load_2d(base + K::kOffZ, &tz, u.h0 * P, (int)(tok0 + (int64_t)(c - 2) * kQ), bar(kZFull));
+                        ++zs;
+                    }
+                    if (c < u.nc) {
+                        const int rs = raw_slot(c);
+                        if (!(ok = wait(kRawEmpty + rs, raw_phase(c) ^ 1)))
+                            break;
+                        // (x's room is free, so the weights of the chunk four before are done with too)
+                        mbar_arrive_expect_tx(bar(kRawFull + rs), K::kXBytes + gbytes);
+                        bulk_load(smem_u32(gate[c % K::kGateSlots]), a.gates + ((id0 + c) * p.H + u.h0) * kGateRec, gbytes, bar(kRawFull + rs));
+                        tma_load_2d(base + (rs ? K::kOffM : K::kOffX), &tx, u.h0 * P, (int)(tok0 + (int64_t)c * kQ) - 3, bar(kRawFull + rs));
+                        ++raws;
+                        if (!SUMMARY) {
+                            const int cs = c % K::kCbBufs;
+                            const uint32_t to = base + K::kOffCb + cs * K::kCbBytes;
+                            if (!(ok = wait(kCbEmpty + cs, ((c / K::kCbBufs) & 1) ^ 1, true)))
+                                break;
+                            mbar_arrive_expect_tx(bar(kCbFull + cs), K::kCbBytes + mbytes);
+                            bulk_load(smem_u32(mask[cs]), a.masks + ((id0 + c) * p.H + u.h0) * kMaskRec, mbytes, bar(kCbFull + cs));
+                            tma_load_2d(to, &tcb, 0, y, bar(kCbFull + cs));
+                            tma_load_2d(to + 4096, &tcb, 0, y + 32, bar(kCbFull + cs));
+                            tma_load_2d(to + 8192, &tcb, 32, y + 32, bar(kCbFull + cs));
+                            ++cbs;
                         }
-                        mbar_arrive_expect_tx(bar(kBcFull + slot), K::kHalf);
-                        for (int k = 0; k < 2 * S / 64; ++k) // boxes of 64 channels: hi, lo
-                            tma_load_2d(base + slot * K::kHalf + k * 8192, &tbc, 64 * k + (part == 0 ? 2 * S : 0), y,
-                                        bar(kBcFull + slot));
-                        used = used < K::kSlots ? used + 1 : K::kSlots;
-                        if (++slot == K::kSlots) {
-                            slot = 0;
-                            ph ^= 1;
-                        }
+                        ok = load_bc(y, 0); // B
                     }
                 }
                 if (!ok) { // gave up: the copies in flight land before the block may end
+                    for (int c = max(cbs - K::kCbBufs, 0); c < cbs; ++c)
+                        mbar_wait_bounded(bar(kCbFull + c % K::kCbBufs), (c / K::kCbBufs) & 1, kDefaultWaitLimit);
+                    if (zs > 0)
+                        mbar_wait_bounded(bar(kZFull), (zs - 1) & 1, kDefaultWaitLimit);
+                    for (int c = max(raws - 2, 0); c < raws; ++c)
+                        if (SUMMARY || c == raws - 1)
+                            mbar_wait_bounded(bar(kRawFull + raw_slot(c)), raw_phase(c), kDefaultWaitLimit);
                     for (int k = 0; k < used; ++k) {
                         if (--slot < 0) {
                             slot = K::kSlots - 1;
@@ -652,9 +697,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             const float D0 = p.D != nullptr ? -kLn2 * __ldg(p.D + u.h0) : 0.f;
             const float D1 = p.D != nullptr && u.nh > 1 ? -kLn2 * __ldg(p.D + u.h0 + 1) : 0.f;
             for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
-                const int mb = c % K::kMBufs, gs = c % K::kGateSlots;
+                const int mb = c % K::kMBufs, cs = c % K::kCbBufs;
                 // the chunk that last had this buffer: its products are done
-                if (!gate_ready(c, true) || !wait_all(kCbFull, c & 1, true) || (c >= K::kMBufs && !i_done(c - K::kMBufs, true)))
+                if (!wait_all(kCbFull + cs, (c / K::kCbBufs) & 1, true) || (c >= K::kMBufs && !i_done(c - K::kMBufs, true)))
                     break;
                 const uint32_t mbuf = base + K::kOffM + mb * K::kMBytes;
                 // 16-blocks (row, column): (0, 0) (3, 0) (3, 1) (3, 2) (3, 3) of one warp, (1, 0) (1, 1) (2, 0)
@@ -664,15 +709,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     const int rb = warp == 2 ? (blk == 0 ? 0 : 3) : (blk < 2 ? 1 : 2);
                     const int i = warp == 2 ? (blk == 0 ? 0 : blk - 1) : (blk < 2 ? blk : blk - 2);
                     const int t = 16 * rb + (lane >> 1), s0 = 16 * i + 8 * odd;
-                    // two boxes of 32 columns, 16-byte pieces swizzled by the row
-                    const uint8_t *cbr = sm + K::kOffCb + (s0 >> 5) * 8192 + t * 128;
+                    // rows of 32 columns (the second half's from row 32 on), 16-byte pieces swizzled by the row
+                    const uint8_t *cbr = sm + K::kOffCb + cs * K::kCbBytes + (t + (s0 >> 5) * 32) * 128;
                     const int piece = (s0 & 31) >> 2;
                     float v[8];
                     *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(cbr + ((piece ^ (t & 7)) << 4));
                     *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(cbr + (((piece + 1) ^ (t & 7)) << 4));
 #pragma unroll
                     for (int h = 0; h < NH; ++h) { // an absent head's mask is never used
-                        const float *rec = gate[gs][h];
+                        const float *rec = mask[cs][h];
                         const float gh = rec[t], gl = rec[64 + t], Dh = h == 0 ? D0 : D1;
                         uint32_t hi[4], lo[4];
 #pragma unroll
@@ -702,64 +747,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 }
                 fence_proxy_async_smem();
                 arrive(kMFull + mb);
-                arrive(kCbEmpty);
-                arrive(kGEmpty + gs);
+                arrive(kCbEmpty + cs);
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        const int part = wg - 1, me = tid - 128;
-        // the summary pass has no z: its room is a second buffer for x
-        auto xoff = [&](int c) { return SUMMARY && (c & 1) ? K::kOffZ : K::kOffX; };
-        const uint32_t zbuf = base + K::kOffZ;
-        const int64_t tok0 = u.start + u.c0 * kQ, ys = (int64_t)p.H * P;
-        // Copies of 128 channels (those of absent heads left out) of a chunk's tokens, from token -3 on for x, to
-        // shared memory, 16 bytes at a time; behind the end of the sequence its last token is taken again.
-        constexpr int PIECES = K::kRow / 16, STEP = kWorkers / PIECES; // a thread keeps its piece of the rows
-        const int piece = me % PIECES, first = me / PIECES;
-        const bool mine = piece < u.nh * (P * (int)sizeof(T) / 16);
-        const uint32_t to = first * K::kRow + 16 * piece;
-        const int64_t xrow = p.xbc_stride * (int64_t)sizeof(T), zrow = p.z_stride * (int64_t)sizeof(T);
-        const char *xat = reinterpret_cast<const char *>(p.xbc) + (tok0 + first - 3) * xrow + u.h0 * P * (int)sizeof(T) + 16 * piece;
-        const char *zat = reinterpret_cast<const char *>(p.z) + (tok0 + first) * zrow + u.h0 * P * (int)sizeof(T) + 16 * piece;
-        auto copy_z = [&](int c) { // chunks in turn: zat is this thread's first row of the next one
-            if (mine) {
-                const int tokens = (int)(u.end - tok0 < (int64_t)(c + 1) * kQ ? u.end - tok0 - (int64_t)c * kQ : kQ);
-#pragma unroll
-                for (int i = 0; i < kQ / STEP; ++i) {
-                    const int t = first + i * STEP;
-                    cp_async16(zbuf + to + i * STEP * K::kRow, zat + (t < tokens ? i * STEP : tokens - 1 - first) * zrow, false);
-                }
-                zat += kQ * zrow;
-            }
-        };
-        auto copy_x = [&](int c) { // likewise, from token -3 on
-            if (mine) {
-                const int tokens = (int)(u.end - tok0 < (int64_t)(c + 1) * kQ ? u.end - tok0 - (int64_t)c * kQ : kQ);
-#pragma unroll
-                for (int i = 0; i < kQ / STEP + 1; ++i) {
-                    const int t = first - 3 + i * STEP;
-                    if (i < kQ / STEP || t < kQ) {
-                        const char *at = xat + (t < tokens ? i * STEP : tokens + 2 - first) * xrow;
-                        bool zeros = false;
-                        if (i == 0 && t < 0 && c == 0) { // before the segment: the window, or the rows of the segment ahead
-                            const T *before = conv_row<T>(p, u.n, u.start, tok0 + t);
-                            zeros = before == nullptr;
-                            at = zeros ? reinterpret_cast<const char *>(p.conv_w)
-                                       : reinterpret_cast<const char *>(before + u.h0 * P) + 16 * piece;
-                        }
-                        cp_async16(base + xoff(c) + to + i * STEP * K::kRow, at, zeros);
-                    }
-                }
-                xat += kQ * xrow;
-            }
-        };
-        if (u.nc > 0)
-            copy_x(0);
-        cp_async_commit();
-        if (SUMMARY && u.nc > 1)
-            copy_x(1);
-        cp_async_commit();
+        const int part = wg - 1;
+        const int64_t ys = (int64_t)p.H * P;
         float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f, wb = 0.f;
         if (live) { // times -log2(e), as the exponential of the SiLU takes its argument
             const float4 w = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + chan);
@@ -810,26 +804,23 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             const bool more = c + 1 < u.nc;
             const int64_t t0 = tok0 + (int64_t)c * kQ; // of chunk c
             // -- x of chunk c + 1: tokens 16 part ..
-            if (SUMMARY)
-                cp_async_wait_but_one(); // (the chunk after it is on its way)
-            else
-                cp_async_wait();
-            group_sync(1, kWorkers); // its rows have landed, and the output of chunk c - 1 has left shared memory
             float x[16];
             if (more) {
-                if (!SUMMARY && c >= 0 && p.z != nullptr)
-                    copy_z(c);
+                const int rs = raw_slot(c + 1);
+                ok = ok && wait_all(kRawFull + rs, raw_phase(c + 1));
                 float r[19]; // tokens -3, .., 15
-                const T *src = reinterpret_cast<const T *>(sm + xoff(c + 1)) + (16 * part) * 128 + row;
+                const T *src = reinterpret_cast<const T *>(sm + (rs ? K::kOffM : K::kOffX)) + (16 * part) * 128 + row;
 #pragma unroll
                 for (int t = 0; t < 19; ++t)
                     r[t] = to_f(src[t * 128]);
-                if (SUMMARY) {
-                    group_sync(1, kWorkers); // every thread has its tokens
-                    if (c + 3 < u.nc)
-                        copy_x(c + 3);
-                    cp_async_commit();
+                if (c < 0 && part == 0 && u.c0 == 0) { // before the sequence: the window
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) {
+                        const T *before = conv_row<T>(p, u.n, u.start, u.start - 3 + t);
+                        r[t] = live && before != nullptr ? to_f(before[chan]) : 0.f;
+                    }
                 }
+                arrive(kRawEmpty + rs);
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     x[t] = silu_scaled(fmaf(w3, r[t + 3], fmaf(w2, r[t + 2], fmaf(w1, r[t + 1], fmaf(w0, r[t], wb)))));
@@ -840,15 +831,12 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         if (t >= valid)
                             x[t] = 0.f;
                 }
-            } else {
-                if (!SUMMARY && c >= 0 && p.z != nullptr)
-                    copy_z(c);
             }
             // -- the state entering chunk c + 1, and x' of that chunk
             if (c >= 0) {
-                ok = ok && wait_all(kUDone, c & 1); // (the gates were waited for as the next chunk's)
+                ok = ok && wait_all(kUDone, c & 1);
                 tc_fence_after();
-                const float gamma = live ? gate[c % K::kGateSlots][hl][256 + 63] : 0.f;
+                const float gamma = live ? gate[c % K::kGateSlots][hl][64 + 63] : 0.f;
                 decay *= gamma;
                 const f2 gg = pack(gamma, gamma);
 #pragma unroll
@@ -875,8 +863,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
                     }
                 }
-                ok = ok && gate_ready(c + 1);
-                const float4 *wt = reinterpret_cast<const float4 *>(gate[(c + 1) % K::kGateSlots][hl] + 192 + 16 * part);
+                const float4 *wt = reinterpret_cast<const float4 *>(gate[(c + 1) % K::kGateSlots][hl] + 16 * part);
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
@@ -890,30 +877,27 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 tc_fence_before();
                 arrive(kHFull);
             }
-            if (SUMMARY) {
-                if (c >= 0)
-                    arrive(kGEmpty + c % K::kGateSlots);
+            if (SUMMARY)
                 continue;
-            }
             // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
             float y[16];
+            uint32_t nf = 0; // the first bad tokens of chunk c, by parts
             if (c >= 0) {
-                ok = ok && i_done(c);
+                ok = ok && i_done(c); // the MMAs waited for kXFull, so the other parts' first bad tokens are here too
+                nf = *reinterpret_cast<const uint32_t *>(bad[c & 1][row]);
                 tc_fence_after();
                 float e[16];
                 tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + 16 * part, y);
                 tmem_ld16(tmem + lanes + K::kYA + 64 * hl + 16 * part, e);
                 tmem_wait_ld();
-                const float4 *eg = reinterpret_cast<const float4 *>(gate[c % K::kGateSlots][hl] + 256 + 16 * part);
+                const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[c % K::kGateSlots][hl] + 64 + 16 * part);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 f = eg[k];
-                    y[4 * k] = fmaf(f.x, y[4 * k], e[4 * k]);
-                    y[4 * k + 1] = fmaf(f.y, y[4 * k + 1], e[4 * k + 1]);
-                    y[4 * k + 2] = fmaf(f.z, y[4 * k + 2], e[4 * k + 2]);
-                    y[4 * k + 3] = fmaf(f.w, y[4 * k + 3], e[4 * k + 3]);
+                for (int k = 0; k < 16; k += 4) {
+                    const ulonglong2 f = eg[k / 4];
+                    const float2 a0 = unpack(fma2(f.x, pack(y[k], y[k + 1]), pack(e[k], e[k + 1])));
+                    const float2 a1 = unpack(fma2(f.y, pack(y[k + 2], y[k + 3]), pack(e[k + 2], e[k + 3])));
+                    y[k] = a0.x; y[k + 1] = a0.y; y[k + 2] = a1.x; y[k + 3] = a1.y;
                 }
-                arrive(kGEmpty + c % K::kGateSlots);
             }
             if (more) {
                 // A non-finite x would reach the tokens before it in its chunk (as 0 times it): the
@@ -942,19 +926,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 tc_fence_before();
                 arrive(kXFull);
             }
-            // the tokens of chunk c + 1 are in every thread's registers, and z of chunk c has landed
-            cp_async_wait();
-            group_sync(1, kWorkers);
-            if (c + 2 < u.nc)
-                copy_x(c + 2);
             if (c < 0)
                 continue;
             // -- the output of chunk c: gate and store
-            const uint32_t nf = *reinterpret_cast<const uint32_t *>(bad[c & 1][row]);
             if (nf != 0x40404040u) {
                 int first = kQ; // the first bad token up to this part's end
                 for (int k = 0; k <= part; ++k)
-                    first = min(first, (int)bad[c & 1][row][k]);
+                    first = min(first, (int)(nf >> (8 * k)) & 0xff);
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     if (16 * part + t >= first)
@@ -964,9 +942,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             // at a time (2-byte stores of a channel took 3400 cycles a chunk)
             T *yr = reinterpret_cast<T *>(smem_raw + (base - smem_u32(smem_raw)) + K::kOffZ) + (16 * part) * 128 + row;
             if (p.z != nullptr) {
+                ok = ok && wait_all(kZFull, c & 1);
 #pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    y[t] *= silu(to_f(yr[t * 128]));
+                for (int t = 0; t < 16; t += 2) {
+                    const float2 v = gated(pack(y[t], y[t + 1]), pack(to_f(yr[t * 128]), to_f(yr[(t + 1) * 128])));
+                    y[t] = v.x;
+                    y[t + 1] = v.y;
+                }
             }
 #pragma unroll
             for (int t = 0; t < 16; t += 2)
@@ -985,8 +967,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         *reinterpret_cast<uint4 *>(dst + i * ys * (int64_t)sizeof(T)) = v;
                 }
             }
+            if (p.z != nullptr) {
+                fence_proxy_async_smem();
+                arrive(kZEmpty);
+            } else {
+                __syncwarp();
+            }
         }
-        cp_async_wait();
         if (ok && SUMMARY) {
             store_state(seg_at(u.seg + 1));
             if (lane == 0 && part == 0 && (q & 1) == 0)
@@ -1058,31 +1045,34 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
     const int tpg = (p.H / p.G * P + 127) / 128;
     const int64_t chunks = max_chunks(p.N, p.batch);
     cudaError_t e = cudaSuccess;
-    ScanArgs a{p, (float *)(ws + l.cb), (float *)(ws + l.gates), (float *)(ws + l.seg), (float *)(ws + l.segdecay), status, p.segments, p.fine, tpg};
+    ScanArgs a{p, (float *)(ws + l.cb), (float *)(ws + l.masks), (float *)(ws + l.gates), (float *)(ws + l.seg), (float *)(ws + l.segdecay), status, p.segments, p.fine, tpg};
     if (p.N > 0) {
         e = cudaFuncSetAttribute(ssm_prep_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem<S>());
         if (e != cudaSuccess)
             return e;
         ssm_prep_kernel<T, S><<<dim3((unsigned)chunks, p.G, 2), kPrepThreads, prep_smem<S>(), s>>>(
-            p, (__nv_bfloat16 *)(ws + l.bc), (float *)(ws + l.cb), (float *)(ws + l.gates), status);
+            p, (__nv_bfloat16 *)(ws + l.bc), (float *)(ws + l.cb), (float *)(ws + l.masks), (float *)(ws + l.gates), status);
         e = record_if(begin, s);
         if (e != cudaSuccess)
             return e;
-        CUtensorMap tbc, tcb;
+        CUtensorMap tbc, tcb, tx, tz{};
+        const CUtensorMapDataType type = sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
         if (!encode_2d(&tbc, ws + l.bc, 4 * S, (uint64_t)chunks * p.G * kQ, 4 * S * 2, 64, kQ, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
-            !encode_2d(&tcb, ws + l.cb, kQ, (uint64_t)chunks * p.G * kQ, kQ * 4, 32, kQ, CU_TENSOR_MAP_SWIZZLE_128B))
+            !encode_2d(&tcb, ws + l.cb, kQ, (uint64_t)chunks * p.G * kQ, kQ * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&tx, p.xbc, p.conv_dim(), p.N, p.xbc_stride * sizeof(T), 128, kQ + 3, CU_TENSOR_MAP_SWIZZLE_NONE, type) ||
+            (p.z != nullptr && !encode_2d(&tz, p.z, (uint64_t)p.H * P, p.N, p.z_stride * sizeof(T), 128, kQ, CU_TENSOR_MAP_SWIZZLE_NONE, type)))
             return cudaErrorInvalidValue;
         if (p.segments > 1) {
             e = cudaFuncSetAttribute(ssm_scan_kernel<T, P, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
             if (e != cudaSuccess)
                 return e;
-            ssm_scan_kernel<T, P, S, true><<<dim3(p.G * tpg, (p.segments - 1) * p.fine, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, a);
+            ssm_scan_kernel<T, P, S, true><<<dim3(p.G * tpg, (p.segments - 1) * p.fine, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, tx, tz, a);
         }
         e = cudaFuncSetAttribute(ssm_scan_kernel<T, P, S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
         if (e != cudaSuccess)
             return e;
-        ssm_scan_kernel<T, P, S, false><<<dim3(p.G * tpg, p.segments, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, a);
+        ssm_scan_kernel<T, P, S, false><<<dim3(p.G * tpg, p.segments, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, tx, tz, a);
         e = cudaGetLastError();
         if (e == cudaSuccess)
             e = record_if(end, s);
