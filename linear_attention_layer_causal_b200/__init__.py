@@ -29,7 +29,7 @@ import ctypes
 import os
 from contextlib import nullcontext
 from dataclasses import dataclass
-from functools import cached_property, lru_cache
+from functools import lru_cache
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -513,18 +513,15 @@ class SsmConfig:
     def conv_dim(self) -> int:
         return self.num_heads * self.head_dim + 2 * self.num_groups * self.state_dim
 
-    @cached_property
-    def _struct(self) -> _SsmConfig:
-        return _SsmConfig(self.num_groups, self.num_heads, self.head_dim, self.state_dim,
-                          self.conv_kernel, self.dt_min, self.dt_max,
-                          GDN_BF16 if self.act_dtype == "bf16" else GDN_F32, self.segments)
-
-    @cached_property
-    def _workspace_sizes(self) -> dict:
-        return {}
-
     def _c(self) -> _SsmConfig:
-        return self._struct
+        return _ssm_struct(self)
+
+
+@lru_cache(maxsize=1024)
+def _ssm_struct(cfg: SsmConfig) -> _SsmConfig:
+    return _SsmConfig(cfg.num_groups, cfg.num_heads, cfg.head_dim, cfg.state_dim, cfg.conv_kernel,
+                      cfg.dt_min, cfg.dt_max, GDN_BF16 if cfg.act_dtype == "bf16" else GDN_F32,
+                      cfg.segments)
 
 
 def _check(name, t, shape, dtype, device, optional=True):
@@ -588,18 +585,14 @@ def _workspace(workspace, need, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+@lru_cache(maxsize=4096)
 def ssm_prefill_workspace_size(cfg: SsmConfig, batch: int, total_tokens: int) -> int:
-    """Bytes of workspace (gdn_ssm_prefill_workspace_size), asked once for each size."""
-    known = cfg._workspace_sizes.get((batch, total_tokens))
-    if known is not None:
-        return known
+    """Bytes of workspace (gdn_ssm_prefill_workspace_size)."""
     n = ctypes.c_size_t(0)
     st = lib().gdn_ssm_prefill_workspace_size(ctypes.byref(cfg._c()), batch, total_tokens,
                                               ctypes.byref(n))
     if st != GDN_OK:
         raise GdnError(st, "gdn_ssm_prefill_workspace_size")
-    if len(cfg._workspace_sizes) < 4096:
-        cfg._workspace_sizes[batch, total_tokens] = n.value
     return n.value
 
 
@@ -632,11 +625,11 @@ def ssm_prefill(cfg: SsmConfig, xbc, dt, cu_seqlens, conv_w, A_log, *, conv_b=No
         zp, zs = _rows("z", z, (N, H, P), act, dev, optional=True)
         need = ssm_prefill_workspace_size(cfg, B, N)
         if y is None:
-            y = torch.empty((N, H, P), dtype=act, device=dev)
+            y = xbc.new_empty(N, H, P)
         if final_state is None and return_final_state:
-            final_state = torch.empty((B, H, P, S), dtype=torch.float32, device=dev)
+            final_state = torch.empty(B, H, P, S, dtype=torch.float32, device=dev)
         if final_conv is None and return_final_conv:
-            final_conv = torch.empty((B, cfg.conv_kernel - 1, C), dtype=act, device=dev)
+            final_conv = xbc.new_empty(B, cfg.conv_kernel - 1, C)
         wp, wb, keep = _workspace(workspace, need, dev)
         state, window = (B, H, P, S), (B, cfg.conv_kernel - 1, C)
         st = lib().gdn_ssm_prefill(
@@ -669,7 +662,7 @@ def ssm_decode(cfg: SsmConfig, xbc, dt, state, conv_cache, conv_w, A_log, *, con
         dp, ds = _rows("dt", dt, (B, H), act, dev)
         zp, zs = _rows("z", z, (B, H, P), act, dev, optional=True)
         if y is None:
-            y = torch.empty((B, H, P), dtype=act, device=dev)
+            y = xbc.new_empty(B, H, P)
         st = lib().gdn_ssm_decode(
             ctypes.byref(cfg._c()), ctypes.byref(_ssm_params(cfg, dev, conv_w, conv_b, A_log, dt_bias, D)),
             xp, xs, dp, ds, zp, zs, _check("state", state, (B, H, P, S), torch.float32, dev, False),
@@ -702,13 +695,13 @@ def _norm_call(x, weight, residual, groups, eps, weight_offset, q, scale, residu
     with on:
         xp, xs = _rows("x", x, shape, act, dev)
         if q is None:
-            q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+            q = torch.empty(rows, dim, dtype=torch.float8_e4m3fn, device=dev)
         if scale is None:
-            scale = torch.empty(blocks, dtype=torch.float32, device=dev)
+            scale = torch.empty(*blocks, dtype=torch.float32, device=dev)
         if residual_out is None and want_r:
-            residual_out = torch.empty(shape, dtype=act, device=dev)
+            residual_out = x.new_empty(rows, dim)
         if y is None and want_y:
-            y = torch.empty(shape, dtype=act, device=dev)
+            y = x.new_empty(rows, dim)
         cfg = _norm_config(rows, dim, groups, eps, weight_offset, GDN_BF16 if act == torch.bfloat16 else GDN_F32)
         st = lib().gdn_rmsnorm_fp8(
             ctypes.byref(cfg), xp, xs, _check("residual", residual, shape, act, dev),
@@ -773,7 +766,7 @@ def matmul_fp8(a, a_scale, w, w_scale, *, out_dtype=None, out=None, workspace=No
         sw = _check("w_scale", w_scale, (-(-N // BLOCK), kb), torch.float32, dev, False)
         wsp, wsb, keep = _workspace(workspace, matmul_fp8_workspace_size(M, N, K), dev)
         if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+            out = torch.empty(M, N, dtype=out_dtype, device=dev)
         op, os_ = _rows("out", out, (M, N), out_dtype, dev)
         st = lib().gdn_matmul_fp8(ap, sa, wp, sw, M, N, K, op, os_,
                                   GDN_BF16 if out_dtype == torch.bfloat16 else GDN_F32, wsp, wsb, s)
