@@ -401,6 +401,9 @@ template <typename T, int P, int S> struct Scan {
     static constexpr uint32_t kYI2 = 448;          // the other buffer of H C^T
 };
 constexpr int kScanThreads = 640;
+// Chunks of the summary pass that are summed in the accumulators before they are added to the state in registers:
+// sums of 12 MMAs a chunk, which are not rounded to the nearest, should stay few.
+constexpr int kSumChunks = 4;
 constexpr uint32_t kTmemCols = 512;
 
 // B and C slots, M buffers, buffers of C B^T and of raw x, and single barriers
@@ -569,7 +572,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 int cbs = 0, raws = 0, zs = 0; // loaded so far
                 bool ok = true;
                 for (int c = 0; ok && c < (SUMMARY ? u.nc : u.nc + 2); ++c) {
-                    const int y = (int)(((id0 + c) * p.G + u.g) * kQ);
+                    const int at = SUMMARY ? u.nc - 1 - c : c; // the summary goes backwards
+                    const int y = (int)(((id0 + at) * p.G + u.g) * kQ);
                     if (!SUMMARY && c < u.nc && !(ok = load_bc(y, 2 * S))) // C
                         break;
                     if (!SUMMARY && c >= 2 && p.z != nullptr) {
@@ -585,8 +589,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             break;
                         // (x's room is free, so the weights of the chunk four before are done with too)
                         mbar_arrive_expect_tx(bar(kRawFull + rs), K::kXBytes + gbytes);
-                        bulk_load(smem_u32(gate[c % K::kGateSlots]), a.gates + ((id0 + c) * p.H + u.h0) * kGateRec, gbytes, bar(kRawFull + rs));
-                        tma_load_2d(base + (rs ? K::kOffM : K::kOffX), &tx, u.h0 * P, (int)(tok0 + (int64_t)c * kQ) - 3, bar(kRawFull + rs));
+                        bulk_load(smem_u32(gate[c % K::kGateSlots]), a.gates + ((id0 + at) * p.H + u.h0) * kGateRec, gbytes, bar(kRawFull + rs));
+                        tma_load_2d(base + (rs ? K::kOffM : K::kOffX), &tx, u.h0 * P, (int)(tok0 + (int64_t)at * kQ) - 3, bar(kRawFull + rs));
                         ++raws;
                         if (!SUMMARY) {
                             const int cs = c % K::kCbBufs;
@@ -631,28 +635,45 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     sph ^= 1;
                 }
             };
-            for (int c = 0; c < u.nc; ++c) {
-                const uint32_t ph = c & 1;
-                if (!SUMMARY) {
-                    ok = wait_all(kBcFull + slot, sph) && wait_all(kHFull, ph);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    // Y: D[row][t] = sum_s H[row][s] C[t][s].  H hi of 16 columns kk sits beside lo in the
-                    // quarter of DH that its warpgroup owns.
-                    const uint32_t ch = base + slot * K::kHalf, cl = ch + S * 128, yi = tmem + (ph ? K::kYI2 : K::kYI);
+            for (int c = 0; SUMMARY && c < u.nc; ++c) {
+                // D[row][s] (+)= sum_t x'[row][t] B[t][s], two buffers of x' and of D
+                ok = wait_all(kBcFull + slot, sph) && wait_all(c & 1 ? kXFull : kHFull, (c >> 1) & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t bh = base + slot * K::kHalf, bl = bh + S * 128, d = tmem + K::kDH + ((c / kSumChunks) & 1) * 128;
 #pragma unroll
-                    for (int kk = 0; kk < S / 16; ++kk) {
-                        const uint32_t hh = tmem + K::kDH + kk / (CW / 16) * CW + kk % (CW / 16) * 8, hlo = hh + CW / 2;
-                        const uint32_t off = kk / 4 * 8192 + kk % 4 * 32;
-                        mma_bf16_ts_if(yi, hh, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), kk > 0, issue);
-                        mma_bf16_ts_if(yi, hh, sdesc_sw128(cl + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
-                        mma_bf16_ts_if(yi, hlo, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
-                    }
-                    mma_commit_if(bar(kBcEmpty + slot), issue);
-                    next_slot();
+                for (int kk = 0; kk < kQ / 16; ++kk) {
+                    const uint32_t xh = tmem + (c & 1 ? K::kX : K::kXP) + 8 * kk, xl = xh + 32;
+                    mma_bf16_ts_if(d, xh, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true),
+                                   kk > 0 || c % kSumChunks > 0, issue);
+                    mma_bf16_ts_if(d, xh, sdesc_sw128(bl + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
+                    mma_bf16_ts_if(d, xl, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
                 }
-                ok = wait_all(kBcFull + slot, sph) && (!SUMMARY || wait_all(kHFull, ph));
+                mma_commit_if(bar(kIDone + (c & 1)), issue);
+                mma_commit_if(bar(kBcEmpty + slot), issue);
+                next_slot();
+            }
+            for (int c = 0; !SUMMARY && c < u.nc; ++c) {
+                const uint32_t ph = c & 1;
+                ok = wait_all(kBcFull + slot, sph) && wait_all(kHFull, ph);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // Y: D[row][t] = sum_s H[row][s] C[t][s].  H hi of 16 columns kk sits beside lo in the
+                // quarter of DH that its warpgroup owns.
+                const uint32_t ch = base + slot * K::kHalf, cl = ch + S * 128, yi = tmem + (ph ? K::kYI2 : K::kYI);
+#pragma unroll
+                for (int kk = 0; kk < S / 16; ++kk) {
+                    const uint32_t hh = tmem + K::kDH + kk / (CW / 16) * CW + kk % (CW / 16) * 8, hlo = hh + CW / 2;
+                    const uint32_t off = kk / 4 * 8192 + kk % 4 * 32;
+                    mma_bf16_ts_if(yi, hh, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), kk > 0, issue);
+                    mma_bf16_ts_if(yi, hh, sdesc_sw128(cl + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
+                    mma_bf16_ts_if(yi, hlo, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
+                }
+                mma_commit_if(bar(kBcEmpty + slot), issue);
+                next_slot();
+                ok = wait_all(kBcFull + slot, sph);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -668,25 +689,23 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 mma_commit_if(bar(kUDone), issue);
                 mma_commit_if(bar(kBcEmpty + slot), issue);
                 next_slot();
-                if (!SUMMARY) {
-                    const int mb = c % K::kMBufs;
-                    ok = wait_all(kXFull, ph) && wait_all(kMFull + mb, (c / K::kMBufs) & 1);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    // I: D[row][64 h + t] = sum_s x[row][s] M_h[t][s]; a head's rows read their own 64 columns.
-                    // The masks are whole, with zeros above the diagonal: leaving the 16-blocks of zeros out by
-                    // smaller MMAs took 3000 cycles instead of 768 (each then waits for the one before it).
-                    const uint32_t mh = base + K::kOffM + mb * K::kMBytes, ml = mh + NH * kQ * kQ * 2;
+                const int mb = c % K::kMBufs;
+                ok = wait_all(kXFull, ph) && wait_all(kMFull + mb, (c / K::kMBufs) & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // I: D[row][64 h + t] = sum_s x[row][s] M_h[t][s]; a head's rows read their own 64 columns.
+                // The masks are whole, with zeros above the diagonal: leaving the 16-blocks of zeros out by
+                // smaller MMAs took 3000 cycles instead of 768 (each then waits for the one before it).
+                const uint32_t mh = base + K::kOffM + mb * K::kMBytes, ml = mh + NH * kQ * kQ * 2;
 #pragma unroll
-                    for (int kk = 0; kk < kQ / 16; ++kk) {
-                        const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
-                        mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), kk > 0, issue);
-                        mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(ml + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
-                        mma_bf16_ts_if(tmem + K::kYA, xl, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
-                    }
-                    mma_commit_if(bar(kIDone + (c & 1)), issue);
+                for (int kk = 0; kk < kQ / 16; ++kk) {
+                    const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
+                    mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), kk > 0, issue);
+                    mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(ml + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
+                    mma_bf16_ts_if(tmem + K::kYA, xl, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
                 }
+                mma_commit_if(bar(kIDone + (c & 1)), issue);
             }
             if (!ok) { // the MMAs in flight end before their memory is given back
                 mma_commit_if(bar(kDrain), issue);
@@ -765,92 +784,152 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         const int tiles = gridDim.x, slots = a.segments * a.fine;
         const int64_t unit0 = ((int64_t)u.n * tiles + u.tile) * slots; // of this sequence and tile in the workspace
         f2 h[CW / 2];
-        auto seg_at = [&](int s) { return a.seg + ((unit0 + s) * 128 + row) * S + CW * part; };
-        auto store_state = [&](float *dst) {
+        // A state of the workspace has its 4-column pieces 128 rows apart, so that a warp's accesses are whole lines
+        // (the caller's have rows of S).
+        constexpr int kApart = 128 * 4;
+        auto seg_at = [&](int s) { return a.seg + (unit0 + s) * 128 * S + CW * part * 128 + row * 4; };
+        auto store_state = [&](float *dst, int apart) {
 #pragma unroll
             for (int i = 0; i < CW / 2; i += 2)
-                *reinterpret_cast<ulonglong2 *>(dst + 2 * i) = make_ulonglong2(h[i], h[i + 1]);
+                *reinterpret_cast<ulonglong2 *>(dst + i / 2 * apart) = make_ulonglong2(h[i], h[i + 1]);
         };
-        auto add_state = [&](const float *src, float d) { // h = d h + src
-            const f2 dd = pack(d, d);
+        auto add_state = [&](const float *src, int apart, float d, float f) { // h = d h + f src
+            const f2 dd = pack(d, d), ff = pack(f, f);
 #pragma unroll
             for (int i = 0; i < CW / 2; i += 2) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(src + 2 * i);
-                h[i] = fma2(dd, h[i], v.x);
-                h[i + 1] = fma2(dd, h[i + 1], v.y);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(src + i / 2 * apart);
+                h[i] = fma2(ff, v.x, mul2(dd, h[i]));
+                h[i + 1] = fma2(ff, v.y, mul2(dd, h[i + 1]));
             }
         };
         const int64_t gstate = (((int64_t)u.n * p.H + u.h0) * P + row) * S + CW * part;
+        bool ok = true; // when a wait gave up, the rest runs without waiting: the outputs are invalid anyway
+        // x of the chunk of tokens t0 .., the i-th that is loaded: tokens 16 part ..
+        auto take_x = [&](int i, int64_t t0, float (&x)[16]) {
+            const int rs = raw_slot(i);
+            ok = ok && wait_all(kRawFull + rs, raw_phase(i));
+            float r[19]; // tokens -3, .., 15
+            const T *src = reinterpret_cast<const T *>(sm + (rs ? K::kOffM : K::kOffX)) + (16 * part) * 128 + row;
+#pragma unroll
+            for (int t = 0; t < 19; ++t)
+                r[t] = to_f(src[t * 128]);
+            if (part == 0 && t0 == u.start) { // before the sequence: the window
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const T *before = conv_row<T>(p, u.n, u.start, u.start - 3 + t);
+                    r[t] = live && before != nullptr ? to_f(before[chan]) : 0.f;
+                }
+            }
+            arrive(kRawEmpty + rs);
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+                x[t] = silu_scaled(fmaf(w3, r[t + 3], fmaf(w2, r[t + 2], fmaf(w1, r[t + 1], fmaf(w0, r[t], wb)))));
+            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part : 0;
+            if (valid < 16) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    if (t >= valid)
+                        x[t] = 0.f;
+            }
+        };
+        // h = f h + the accumulator at column `at`
+        auto add_acc = [&](float f, uint32_t at) {
+            const f2 ff = pack(f, f);
+#pragma unroll
+            for (int i = 0; i < CW; i += 16) {
+                float v[16];
+                tmem_ld16(tmem + lanes + at + CW * part + i, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    h[i / 2 + k] = fma2(ff, h[i / 2 + k], pack(v[2 * k], v[2 * k + 1]));
+            }
+        };
 #pragma unroll
         for (int i = 0; i < CW / 2; ++i)
             h[i] = 0ull;
-        if (SUMMARY || slots == 1) {
-            if (u.seg == 0 && live && p.init_state != nullptr)
-                add_state(p.init_state + gstate, 0.f);
-            if (SUMMARY && u.seg == 0)
-                store_state(seg_at(0)); // the output pass must not read what it may be asked to overwrite
-        } else {
-            // state 1 is the end of the first summary segment; each later one is its segment's own part
-            const int to = u.seg * a.fine;
-            add_state(seg_at(to > 0 ? 1 : 0), 0.f);
-#pragma unroll 1
-            for (int s = 2; s <= to; ++s)
-                add_state(seg_at(s), a.segdecay[(unit0 + s - 1) * 2 + hl]);
-        }
-        float decay = 1.f;
-        bool ok = true; // when a wait gave up, the rest runs without waiting: every warp still meets the others
-#pragma unroll 1
-        for (int c = -1; c < u.nc; ++c) {
-            const bool more = c + 1 < u.nc;
-            const int64_t t0 = tok0 + (int64_t)c * kQ; // of chunk c
-            // -- x of chunk c + 1: tokens 16 part ..
-            float x[16];
-            if (more) {
-                const int rs = raw_slot(c + 1);
-                ok = ok && wait_all(kRawFull + rs, raw_phase(c + 1));
-                float r[19]; // tokens -3, .., 15
-                const T *src = reinterpret_cast<const T *>(sm + (rs ? K::kOffM : K::kOffX)) + (16 * part) * 128 + row;
+        if (SUMMARY) {
+            if (u.seg == 0) { // the output pass must not read what it may be asked to overwrite
+                if (live && p.init_state != nullptr)
+                    add_state(p.init_state + gstate, 4, 0.f, 1.f);
+                store_state(seg_at(0), kApart);
 #pragma unroll
-                for (int t = 0; t < 19; ++t)
-                    r[t] = to_f(src[t * 128]);
-                if (c < 0 && part == 0 && u.c0 == 0) { // before the sequence: the window
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) {
-                        const T *before = conv_row<T>(p, u.n, u.start, u.start - 3 + t);
-                        r[t] = live && before != nullptr ? to_f(before[chan]) : 0.f;
-                    }
-                }
-                arrive(kRawEmpty + rs);
-#pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    x[t] = silu_scaled(fmaf(w3, r[t + 3], fmaf(w2, r[t + 2], fmaf(w1, r[t + 1], fmaf(w0, r[t], wb)))));
-                const int valid = live ? (int)(u.end - t0 - kQ < kQ ? u.end - t0 - kQ : kQ) - 16 * part : 0;
-                if (valid < 16) {
-#pragma unroll
-                    for (int t = 0; t < 16; ++t)
-                        if (t >= valid)
-                            x[t] = 0.f;
-                }
+                for (int i = 0; i < CW / 2; ++i)
+                    h[i] = 0ull;
             }
-            // -- the state entering chunk c + 1, and x' of that chunk
-            if (c >= 0) {
-                ok = ok && wait_all(kUDone, c & 1);
+            // Backwards, so that the decay from a chunk to the segment's end is known when its x' is made: the
+            // chunks' shares are then summed as they are, kSumChunks of them in the accumulators.
+            float decay = 1.f;
+#pragma unroll 1
+            for (int c = 0; c < u.nc; ++c) {
+                float x[16];
+                take_x(c, tok0 + (int64_t)(u.nc - 1 - c) * kQ, x);
+                if (c >= 2) {
+                    ok = ok && i_done(c - 2);
+                    tc_fence_after();
+                    if (c % kSumChunks == 1)
+                        add_acc(1.f, K::kDH + ((c / kSumChunks - 1) & 1) * 128);
+                }
+                const float *rec = gate[c % K::kGateSlots][hl];
+                const float4 *wt = reinterpret_cast<const float4 *>(rec + 16 * part);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    const float4 w = wt[k / 2];
+                    split2(x[2 * k] * (w.x * decay), x[2 * k + 1] * (w.y * decay), hi[k], lo[k]);
+                    split2(x[2 * k + 2] * (w.z * decay), x[2 * k + 3] * (w.w * decay), hi[k + 1], lo[k + 1]);
+                }
+                decay *= live ? rec[64 + 63] : 0.f;
+                const uint32_t to = tmem + lanes + (c & 1 ? K::kX : K::kXP) + 8 * part;
+                tmem_st8(to, hi);
+                tmem_st8(to + 32, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(c & 1 ? kXFull : kHFull);
+            }
+            if (u.nc > 0) {
+                ok = ok && i_done(u.nc - 1);
                 tc_fence_after();
-                const float gamma = live ? gate[c % K::kGateSlots][hl][64 + 63] : 0.f;
-                decay *= gamma;
-                const f2 gg = pack(gamma, gamma);
-#pragma unroll
-                for (int i = 0; i < CW; i += 16) {
-                    float v[16];
-                    tmem_ld16(tmem + lanes + K::kDH + CW * part + i, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        h[i / 2 + k] = fma2(gg, h[i / 2 + k], pack(v[2 * k], v[2 * k + 1]));
-                }
+                const int last = (u.nc - 1) / kSumChunks;
+                if ((u.nc - 1) % kSumChunks == 0 && last > 0)
+                    add_acc(1.f, K::kDH + ((last - 1) & 1) * 128);
+                add_acc(1.f, K::kDH + (last & 1) * 128);
             }
-            if (more) {
-                if (!SUMMARY) {
+            if (u.seg == 0 && live && p.init_state != nullptr)
+                add_state(p.init_state + gstate, 4, 1.f, decay);
+            if (ok) {
+                store_state(seg_at(u.seg + 1), kApart);
+                if (lane == 0 && part == 0 && (q & 1) == 0)
+                    a.segdecay[(unit0 + u.seg) * 2 + hl] = decay;
+            }
+        } else {
+            if (slots == 1) {
+                if (live && p.init_state != nullptr)
+                    add_state(p.init_state + gstate, 4, 0.f, 1.f);
+            } else {
+                // state 1 is the end of the first summary segment; each later one is its segment's own part
+                const int to = u.seg * a.fine;
+                add_state(seg_at(to > 0 ? 1 : 0), kApart, 0.f, 1.f);
+#pragma unroll 1
+                for (int s = 2; s <= to; ++s)
+                    add_state(seg_at(s), kApart, a.segdecay[(unit0 + s - 1) * 2 + hl], 1.f);
+            }
+#pragma unroll 1
+            for (int c = -1; c < u.nc; ++c) {
+                const bool more = c + 1 < u.nc;
+                const int64_t t0 = tok0 + (int64_t)c * kQ; // of chunk c
+                // -- x of chunk c + 1: tokens 16 part ..
+                float x[16];
+                if (more)
+                    take_x(c + 1, t0 + kQ, x);
+                // -- the state entering chunk c + 1, and x' of that chunk
+                if (c >= 0) {
+                    ok = ok && wait_all(kUDone, c & 1);
+                    tc_fence_after();
+                    const float gamma = live ? gate[c % K::kGateSlots][hl][64 + 63] : 0.f;
+                    add_acc(gamma, K::kDH);
+                }
+                if (more) {
 #pragma unroll
                     for (int i = 0; i < CW; i += 16) {
                         uint32_t hi[8], lo[8];
@@ -862,124 +941,117 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
                         tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
                     }
+                    const float4 *wt = reinterpret_cast<const float4 *>(gate[(c + 1) % K::kGateSlots][hl] + 16 * part);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        const float4 w = wt[k / 2];
+                        split2(x[2 * k] * w.x, x[2 * k + 1] * w.y, hi[k], lo[k]);
+                        split2(x[2 * k + 2] * w.z, x[2 * k + 3] * w.w, hi[k + 1], lo[k + 1]);
+                    }
+                    tmem_st8(tmem + lanes + K::kXP + 8 * part, hi);
+                    tmem_st8(tmem + lanes + K::kXP + 32 + 8 * part, lo);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive(kHFull);
                 }
-                const float4 *wt = reinterpret_cast<const float4 *>(gate[(c + 1) % K::kGateSlots][hl] + 16 * part);
-                uint32_t hi[8], lo[8];
+                // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
+                float y[16];
+                uint32_t nf = 0; // the first bad tokens of chunk c, by parts
+                if (c >= 0) {
+                    ok = ok && i_done(c); // the MMAs waited for kXFull, so the other parts' first bad tokens are here too
+                    nf = *reinterpret_cast<const uint32_t *>(bad[c & 1][row]);
+                    tc_fence_after();
+                    float e[16];
+                    tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + 16 * part, y);
+                    tmem_ld16(tmem + lanes + K::kYA + 64 * hl + 16 * part, e);
+                    tmem_wait_ld();
+                    const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[c % K::kGateSlots][hl] + 64 + 16 * part);
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    const float4 w = wt[k / 2];
-                    split2(x[2 * k] * w.x, x[2 * k + 1] * w.y, hi[k], lo[k]);
-                    split2(x[2 * k + 2] * w.z, x[2 * k + 3] * w.w, hi[k + 1], lo[k + 1]);
+                    for (int k = 0; k < 16; k += 4) {
+                        const ulonglong2 f = eg[k / 4];
+                        const float2 a0 = unpack(fma2(f.x, pack(y[k], y[k + 1]), pack(e[k], e[k + 1])));
+                        const float2 a1 = unpack(fma2(f.y, pack(y[k + 2], y[k + 3]), pack(e[k + 2], e[k + 3])));
+                        y[k] = a0.x; y[k + 1] = a0.y; y[k + 2] = a1.x; y[k + 3] = a1.y;
+                    }
                 }
-                tmem_st8(tmem + lanes + K::kXP + 8 * part, hi);
-                tmem_st8(tmem + lanes + K::kXP + 32 + 8 * part, lo);
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(kHFull);
-            }
-            if (SUMMARY)
-                continue;
-            // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
-            float y[16];
-            uint32_t nf = 0; // the first bad tokens of chunk c, by parts
-            if (c >= 0) {
-                ok = ok && i_done(c); // the MMAs waited for kXFull, so the other parts' first bad tokens are here too
-                nf = *reinterpret_cast<const uint32_t *>(bad[c & 1][row]);
-                tc_fence_after();
-                float e[16];
-                tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + 16 * part, y);
-                tmem_ld16(tmem + lanes + K::kYA + 64 * hl + 16 * part, e);
-                tmem_wait_ld();
-                const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[c % K::kGateSlots][hl] + 64 + 16 * part);
+                if (more) {
+                    // A non-finite x would reach the tokens before it in its chunk (as 0 times it): the
+                    // product takes 0 instead, and the output is set from that token on.
+                    float zero = 0.f;
 #pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                    const ulonglong2 f = eg[k / 4];
-                    const float2 a0 = unpack(fma2(f.x, pack(y[k], y[k + 1]), pack(e[k], e[k + 1])));
-                    const float2 a1 = unpack(fma2(f.y, pack(y[k + 2], y[k + 3]), pack(e[k + 2], e[k + 3])));
-                    y[k] = a0.x; y[k + 1] = a0.y; y[k + 2] = a1.x; y[k + 3] = a1.y;
+                    for (int t = 0; t < 16; ++t)
+                        zero = fmaf(x[t], 0.f, zero);
+                    int first = kQ;
+                    if (zero != 0.f) {
+#pragma unroll
+                        for (int t = 15; t >= 0; --t)
+                            if (!(fabsf(x[t]) <= 3.402823466e38f)) {
+                                first = 16 * part + t;
+                                x[t] = 0.f;
+                            }
+                    }
+                    bad[(c + 1) & 1][row][part] = (uint8_t)first;
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+                    tmem_st8(tmem + lanes + K::kX + 8 * part, hi);
+                    tmem_st8(tmem + lanes + K::kX + 32 + 8 * part, lo);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive(kXFull);
                 }
-            }
-            if (more) {
-                // A non-finite x would reach the tokens before it in its chunk (as 0 times it): the
-                // product takes 0 instead, and the output is set from that token on.
-                float zero = 0.f;
+                if (c < 0)
+                    continue;
+                // -- the output of chunk c: gate and store
+                if (nf != 0x40404040u) {
+                    int first = kQ; // the first bad token up to this part's end
+                    for (int k = 0; k <= part; ++k)
+                        first = min(first, (int)(nf >> (8 * k)) & 0xff);
 #pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    zero = fmaf(x[t], 0.f, zero);
-                int first = kQ;
-                if (zero != 0.f) {
-#pragma unroll
-                    for (int t = 15; t >= 0; --t)
-                        if (!(fabsf(x[t]) <= 3.402823466e38f)) {
-                            first = 16 * part + t;
-                            x[t] = 0.f;
-                        }
+                    for (int t = 0; t < 16; ++t)
+                        if (16 * part + t >= first)
+                            y[t] = __uint_as_float(0x7fffffffu);
                 }
-                bad[(c + 1) & 1][row][part] = (uint8_t)first;
-                uint32_t hi[8], lo[8];
+                // through shared memory, over z where there is one, so that a warp stores its 32 channels of 8 tokens
+                // at a time (2-byte stores of a channel took 3400 cycles a chunk)
+                T *yr = reinterpret_cast<T *>(smem_raw + (base - smem_u32(smem_raw)) + K::kOffZ) + (16 * part) * 128 + row;
+                if (p.z != nullptr) {
+                    ok = ok && wait_all(kZFull, c & 1);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
-                tmem_st8(tmem + lanes + K::kX + 8 * part, hi);
-                tmem_st8(tmem + lanes + K::kX + 32 + 8 * part, lo);
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(kXFull);
-            }
-            if (c < 0)
-                continue;
-            // -- the output of chunk c: gate and store
-            if (nf != 0x40404040u) {
-                int first = kQ; // the first bad token up to this part's end
-                for (int k = 0; k <= part; ++k)
-                    first = min(first, (int)(nf >> (8 * k)) & 0xff);
-#pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    if (16 * part + t >= first)
-                        y[t] = __uint_as_float(0x7fffffffu);
-            }
-            // through shared memory, over z where there is one, so that a warp stores its 32 channels of 8 tokens
-            // at a time (2-byte stores of a channel took 3400 cycles a chunk)
-            T *yr = reinterpret_cast<T *>(smem_raw + (base - smem_u32(smem_raw)) + K::kOffZ) + (16 * part) * 128 + row;
-            if (p.z != nullptr) {
-                ok = ok && wait_all(kZFull, c & 1);
-#pragma unroll
-                for (int t = 0; t < 16; t += 2) {
-                    const float2 v = gated(pack(y[t], y[t + 1]), pack(to_f(yr[t * 128]), to_f(yr[(t + 1) * 128])));
-                    y[t] = v.x;
-                    y[t + 1] = v.y;
+                    for (int t = 0; t < 16; t += 2) {
+                        const float2 v = gated(pack(y[t], y[t + 1]), pack(to_f(yr[t * 128]), to_f(yr[(t + 1) * 128])));
+                        y[t] = v.x;
+                        y[t + 1] = v.y;
+                    }
                 }
-            }
 #pragma unroll
-            for (int t = 0; t < 16; t += 2)
-                put2(yr + t * 128, yr + (t + 1) * 128, y[t], y[t + 1]);
-            __syncwarp();
-            if (live) {
-                constexpr int LANES = 2 * (int)sizeof(T), ROWS = 32 / LANES; // lanes of a row's 32 channels, rows at once
-                const int valid = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part;
-                const int t = lane / LANES, k = lane % LANES;
-                const uint8_t *from = sm + K::kOffZ + (16 * part + t) * K::kRow + 32 * q * (int)sizeof(T) + 16 * k;
-                char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + (t0 + 16 * part + t) * ys + u.h0 * P + 32 * q) + 16 * k;
-#pragma unroll
-                for (int i = 0; i < 16; i += ROWS) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(from + i * K::kRow);
-                    if (t + i < valid)
-                        *reinterpret_cast<uint4 *>(dst + i * ys * (int64_t)sizeof(T)) = v;
-                }
-            }
-            if (p.z != nullptr) {
-                fence_proxy_async_smem();
-                arrive(kZEmpty);
-            } else {
+                for (int t = 0; t < 16; t += 2)
+                    put2(yr + t * 128, yr + (t + 1) * 128, y[t], y[t + 1]);
                 __syncwarp();
+                if (live) {
+                    constexpr int LANES = 2 * (int)sizeof(T), ROWS = 32 / LANES; // lanes of a row's 32 channels, rows at once
+                    const int valid = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part;
+                    const int t = lane / LANES, k = lane % LANES;
+                    const uint8_t *from = sm + K::kOffZ + (16 * part + t) * K::kRow + 32 * q * (int)sizeof(T) + 16 * k;
+                    char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + (t0 + 16 * part + t) * ys + u.h0 * P + 32 * q) + 16 * k;
+#pragma unroll
+                    for (int i = 0; i < 16; i += ROWS) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(from + i * K::kRow);
+                        if (t + i < valid)
+                            *reinterpret_cast<uint4 *>(dst + i * ys * (int64_t)sizeof(T)) = v;
+                    }
+                }
+                if (p.z != nullptr) {
+                    fence_proxy_async_smem();
+                    arrive(kZEmpty);
+                } else {
+                    __syncwarp();
+                }
             }
-        }
-        if (ok && SUMMARY) {
-            store_state(seg_at(u.seg + 1));
-            if (lane == 0 && part == 0 && (q & 1) == 0)
-                a.segdecay[(unit0 + u.seg) * 2 + hl] = decay;
-        } else if (ok && u.seg == a.segments - 1 && live && p.final_state != nullptr) {
-            store_state(p.final_state + gstate);
+            if (ok && u.seg == a.segments - 1 && live && p.final_state != nullptr)
+                store_state(p.final_state + gstate, 4);
         }
     }
     __syncwarp();
@@ -1010,8 +1082,8 @@ template <typename T> __global__ void __launch_bounds__(256) ssm_final_conv_kern
 
 // The cut of the sequences: segments of the output pass, and how many parts the
 // summary pass before it cuts each into.  Costs are the chunks of the busiest
-// SM; a chunk of the summary pass (no output) is about half of one of the
-// output pass, and the pass itself about three chunks.
+// SM; a chunk of the summary pass (no output) takes 1.2 us where one of the
+// output pass takes 4.3, and the pass itself about as long as three of those.
 struct Cut {
     int segments, fine;
 };
@@ -1027,7 +1099,7 @@ Cut choose_cut(const gdn_ssm_config *c, int64_t N, int batch) {
             break;
         for (int f = 1; f <= 4 && s * f <= kMaxSegments && (f == 1 || L / (s * f) >= 4); ++f) {
             const double t = (double)(waves(units * s) * ((L + s - 1) / s)) +
-                             (s > 1 ? 3.0 + 0.5 * (double)(waves(units * f * (s - 1)) * ((L + s * f - 1) / (s * f))) : 0.0);
+                             (s > 1 ? 3.0 + 0.28 * (double)(waves(units * f * (s - 1)) * ((L + s * f - 1) / (s * f))) : 0.0);
             if ((c->segments > 0 && f == 1) || t < 0.95 * cost) {
                 best = Cut{s, s > 1 ? f : 1};
                 cost = t;
