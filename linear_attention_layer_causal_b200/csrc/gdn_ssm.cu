@@ -388,10 +388,13 @@ template <typename T, int P, int S> struct Scan {
     static constexpr int kCbBufs = kMBufs;
     static constexpr int kCbBytes = 3 * 32 * 32 * 4;  // C B^T without its upper right quarter
     static constexpr int kRow = 128 * sizeof(T);      // 128 channels of a token
-    static constexpr int kXBytes = (kQ + 3) * kRow;   // x; the summary pass has its second buffer where M is
+    static constexpr int kXBytes = (kQ + 3) * kRow;   // x
     static constexpr int kOffM = kSlots * kHalf, kOffCb = kOffM + kMBufs * kMBytes, kOffX = kOffCb + kCbBufs * kCbBytes,
                          kOffZ = kOffX + kXBytes;
-    static constexpr size_t kSmem = 1024 + kOffZ + kQ * kRow;
+    // the summary pass's second buffer of x: over M and C B^T where it fits, else from z's room on
+    static constexpr bool kOverM = kMBufs * kMBytes + kCbBufs * kCbBytes >= kXBytes;
+    static constexpr int kOffX2 = kOverM ? kOffM : kOffZ;
+    static constexpr size_t kSmem = 1024 + kOffZ + (kOverM ? kQ * kRow : kXBytes);
     // TMEM columns
     static constexpr uint32_t kDH = 0;             // x' B^T, then H hi and lo of the next chunk
     static constexpr uint32_t kYI = 128;           // H C^T
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     };
     auto i_done = [&](int c, bool patient = false) { return wait_all(kIDone + (c & 1), (c >> 1) & 1, patient); };
     const int64_t tok0 = u.start + u.c0 * kQ;
-    // raw x: the summary pass has no M, whose room is its second buffer
+    // raw x: the summary pass has two buffers
     auto raw_slot = [](int c) { return SUMMARY ? c & 1 : 0; };
     auto raw_phase = [](int c) { return (uint32_t)(SUMMARY ? c >> 1 : c) & 1; };
     const int row = 32 * q + lane;          // a worker thread's state row
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         // (x's room is free, so the weights of the chunk four before are done with too)
                         mbar_arrive_expect_tx(bar(kRawFull + rs), K::kXBytes + gbytes);
                         bulk_load(smem_u32(gate[c % K::kGateSlots]), a.gates + ((id0 + at) * p.H + u.h0) * kGateRec, gbytes, bar(kRawFull + rs));
-                        tma_load_2d(base + (rs ? K::kOffM : K::kOffX), &tx, u.h0 * P, (int)(tok0 + (int64_t)at * kQ) - 3, bar(kRawFull + rs));
+                        tma_load_2d(base + (rs ? K::kOffX2 : K::kOffX), &tx, u.h0 * P, (int)(tok0 + (int64_t)at * kQ) - 3, bar(kRawFull + rs));
                         ++raws;
                         if (!SUMMARY) {
                             const int cs = c % K::kCbBufs;
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             const int rs = raw_slot(i);
             ok = ok && wait_all(kRawFull + rs, raw_phase(i));
             float r[19]; // tokens -3, .., 15
-            const T *src = reinterpret_cast<const T *>(sm + (rs ? K::kOffM : K::kOffX)) + (16 * part) * 128 + row;
+            const T *src = reinterpret_cast<const T *>(sm + (rs ? K::kOffX2 : K::kOffX)) + (16 * part) * 128 + row;
 #pragma unroll
             for (int t = 0; t < 19; ++t)
                 r[t] = to_f(src[t * 128]);

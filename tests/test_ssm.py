@@ -528,3 +528,16 @@ def test_prefill_and_decode_past_32_bit_offsets():
     assert torch.equal(conv[-1:], C1)
     for a, b in ((state[-1], S1[0]), (y[-1].float(), y1[0].float())):
         assert float((a - b).norm()) <= 2.0 ** -8 * float(b.norm())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("segments", [2, 7])
+@pytest.mark.parametrize("P", [64, 128])
+@pytest.mark.parametrize("S", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_segments_of_every_layout(dtype, S, P, segments):
+    """Long segments (several chunks, so several buffers in use at once) of every kernel the library has."""
+    lens = [1000, 70, 460]
+    cfg = gdn.SsmConfig(2, 6, P, S, act_dtype=dtype, segments=segments)
+    d, cu = make(cfg, lens, 30 + segments, wide=True)
+    check(cfg, d, lens, prefill(cfg, d, cu, return_final_state=True, return_final_conv=True))
