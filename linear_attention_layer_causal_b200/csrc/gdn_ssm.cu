@@ -18,8 +18,8 @@
 // With few sequences each is cut into segments, and a first run of the scan
 // kernel, without outputs, finds what each segment adds to the state.
 //
-// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 206 us (prep
-// 28, summary 41, output pass 148), where moving the bytes would take 35 and
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 199 us (prep
+// 28, summary about 26, output pass 145), where moving the bytes would take 35 and
 // the MMAs 50.  What bounds it is the 16 warps' instructions: about 8000 cycles
 // a chunk (21000 instructions on 4 schedulers: the splits, the convolution, two
 // SiLUs), of which the tensor core is busy 2300.
@@ -29,6 +29,8 @@
 // 2^-17 of each term, where single bfloat16 operands would put 2^-9 on the
 // float32 state.  Log-decays are summed in 64 bits and M takes their difference
 // as two floats: at G = -1000 one float's step alone is 6e-5.
+#include <algorithm>
+
 #include "gdn_sm100.cuh"
 #include "gdn_ssm.cuh"
 #include "gdn_tmap.h"
@@ -454,8 +456,8 @@ struct ScanArgs {
 // role per warpgroup instead (x, state, output) every role was one or two warps
 // of a scheduler, too few to hide their own latencies.  They meet only through
 // the mbarriers of what they share, so that a warp in its exponentials runs
-// beside one in its splits (with two meetings of all 16 a chunk: 227 us for the
-// 206 above, with copies of x and z by their own threads).
+// beside one in its splits (with two meetings of all 16 a chunk, and copies of x
+// and z by their own threads, the output pass took 160 us for 145).
 // SUMMARY: only the states of the segments but the last, from zero (the first
 // from the initial state, which is also copied); no output.
 template <typename T, int P, int S, bool SUMMARY>
@@ -1084,27 +1086,39 @@ template <typename T> __global__ void __launch_bounds__(256) ssm_final_conv_kern
 }
 
 // The cut of the sequences: segments of the output pass, and how many parts the
-// summary pass before it cuts each into.  Costs are the chunks of the busiest
-// SM; a chunk of the summary pass (no output) takes 1.2 us where one of the
-// output pass takes 4.3, and the pass itself about as long as three of those.
+// summary pass before it cuts each into.  The lengths are on the device, so that
+// the choice knows their sum only; of several sequences the longest is taken to
+// have 2.3 times the mean (that of five cut at random).  Costs are in chunks of
+// the output pass, 4.3 us: a chunk of the summary pass takes 1.2 us, a block
+// about 6 us to start and end, the summary pass 13 us by itself.
+// Measured with 32 heads of 64 and 128 states, 1 and the chosen number of
+// segments: 1024 tokens 84 and 49 us (8); 4096, 64, 64, 64 tokens 262 and 119
+// (4); 512, 512 57 and 48 (4); what it costs where the lengths are alike after
+// all: four of 700 tokens 69 and 78 (4).
 struct Cut {
     int segments, fine;
 };
-int64_t waves(int64_t blocks) { return (blocks + kSMs - 1) / kSMs; }
 Cut choose_cut(const gdn_ssm_config *c, int64_t N, int batch) {
-    const int64_t units = (int64_t)batch * c->num_groups * (((int64_t)(c->num_heads / c->num_groups) * c->head_dim + 127) / 128);
+    const int64_t tiles = c->num_groups * (((int64_t)(c->num_heads / c->num_groups) * c->head_dim + 127) / 128);
     const int64_t L = batch > 0 ? (N / batch + kQ - 1) / kQ : 0;
+    const double all = (double)tiles * ((double)N / kQ + 0.5 * batch); // chunks
+    const double longest = batch > 1 ? (double)std::min<int64_t>(N, N / batch * 23 / 10) / kQ + 0.5 : (double)L;
+    // `share` of the chunks in `blocks` blocks, the longest sequence's in `parts`
+    const auto run = [&](double share, int64_t blocks, int parts) {
+        const double one = batch > 1 ? longest / parts : (double)((L + parts - 1) / parts);
+        return batch > 1 ? std::max(one, share * all / kSMs + 0.5 * one) : one * (double)((blocks + kSMs - 1) / kSMs);
+    };
     Cut best{1, 1};
-    double cost = (double)(waves(units) * L);
-    const int from = c->segments > 0 ? c->segments : 2, to = c->segments > 0 ? c->segments : kMaxSegments;
-    for (int s = from; s <= to; ++s) {
-        if (c->segments == 0 && L / s < 4)
-            break;
-        for (int f = 1; f <= 4 && s * f <= kMaxSegments && (f == 1 || L / (s * f) >= 4); ++f) {
-            const double t = (double)(waves(units * s) * ((L + s - 1) / s)) +
-                             (s > 1 ? 3.0 + 0.28 * (double)(waves(units * f * (s - 1)) * ((L + s * f - 1) / (s * f))) : 0.0);
-            if ((c->segments > 0 && f == 1) || t < 0.95 * cost) {
-                best = Cut{s, s > 1 ? f : 1};
+    double cost = 0.0;
+    const int from = c->segments > 0 ? c->segments : 1, to = c->segments > 0 ? c->segments : kMaxSegments;
+    for (int s = from; s <= to && (s == from || L / s >= 2); ++s) {
+        const int64_t blocks = tiles * batch * s;
+        for (int f = 1; f <= (s > 1 ? 4 : 1) && s * f <= kMaxSegments && (f == 1 || L / (s * f) >= 4); ++f) {
+            double t = run(1.0, blocks, s) + 1.5 * (double)blocks / kSMs;
+            if (s > 1)
+                t += 3.0 + 0.28 * run((double)(s - 1) / s, tiles * batch * (s - 1) * f, s * f);
+            if ((s == from && f == 1) || t < 0.95 * cost) {
+                best = Cut{s, f};
                 cost = t;
             }
         }
