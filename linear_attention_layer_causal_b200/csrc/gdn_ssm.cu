@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
     constexpr int LDS = S + 8; // row length in shared memory: rows 16 bytes apart in banks
     const int64_t id = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;"); // the scan kernel's blocks may set up beside the last of these
     if (id == 0 && g == 0 && blockIdx.z == 0 && tid == 0)
         status[0] = status[1] = 0;
     // the sequence of this chunk number: the last n with first_chunk(cu[n]) <= id
@@ -516,6 +517,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    // Everything above may run beside the prep kernel, what follows reads its results (a short prompt 13.0 us for
+    // 15.6).  A summary pass does not let the output pass set up beside it: a long document took 378 us for 350.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     // A wait that runs out (about a second) makes every role stop at its next
     // wait; what is in flight is waited for before the block ends.
@@ -1141,7 +1145,9 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
             return e;
         ssm_prep_kernel<T, S><<<dim3((unsigned)chunks, p.G, 2), kPrepThreads, prep_smem<S>(), s>>>(
             p, (__nv_bfloat16 *)(ws + l.bc), (float *)(ws + l.cb), (float *)(ws + l.masks), (float *)(ws + l.gates), status);
-        e = record_if(begin, s);
+        e = cudaGetLastError();
+        if (e == cudaSuccess)
+            e = record_if(begin, s);
         if (e != cudaSuccess)
             return e;
         CUtensorMap tbc, tcb, tx, tz{};
@@ -1152,17 +1158,31 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
             !encode_2d(&tx, p.xbc, p.conv_dim(), p.N, p.xbc_stride * sizeof(T), 128, kQ + 3, CU_TENSOR_MAP_SWIZZLE_NONE, type) ||
             (p.z != nullptr && !encode_2d(&tz, p.z, (uint64_t)p.H * P, p.N, p.z_stride * sizeof(T), 128, kQ, CU_TENSOR_MAP_SWIZZLE_NONE, type)))
             return cudaErrorInvalidValue;
+        const auto launch_after = [&](auto kernel, int segments) { // its start may be beside the end of the kernel before it
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(p.G * tpg, segments, p.batch);
+            cfg.blockDim = dim3(kScanThreads);
+            cfg.dynamicSmemBytes = K::kSmem;
+            cfg.stream = s;
+            cudaLaunchAttribute at{};
+            at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at.val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            return cudaLaunchKernelEx(&cfg, kernel, tbc, tcb, tx, tz, a);
+        };
         if (p.segments > 1) {
             e = cudaFuncSetAttribute(ssm_scan_kernel<T, P, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
             if (e != cudaSuccess)
                 return e;
-            ssm_scan_kernel<T, P, S, true><<<dim3(p.G * tpg, (p.segments - 1) * p.fine, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, tx, tz, a);
+            e = launch_after(ssm_scan_kernel<T, P, S, true>, (p.segments - 1) * p.fine);
+            if (e != cudaSuccess)
+                return e;
         }
         e = cudaFuncSetAttribute(ssm_scan_kernel<T, P, S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
         if (e != cudaSuccess)
             return e;
-        ssm_scan_kernel<T, P, S, false><<<dim3(p.G * tpg, p.segments, p.batch), kScanThreads, K::kSmem, s>>>(tbc, tcb, tx, tz, a);
-        e = cudaGetLastError();
+        e = launch_after(ssm_scan_kernel<T, P, S, false>, p.segments);
         if (e == cudaSuccess)
             e = record_if(end, s);
         return e;
