@@ -208,9 +208,9 @@ GDN_API gdn_status gdn_prefill_status(const void *workspace, size_t workspace_by
 
 /*
  * Testing hook for the bounded waits above.  Arms a one-shot on the calling
- * host thread: the next gdn_prefill or gdn_prefill_noalloc call made by this
- * thread gives each wait between the warps of its chunked kernel `cycles` SM
- * cycles instead of the default of 2e9 (about one second), so that a test can
+ * host thread: the next gdn_prefill, gdn_prefill_noalloc, gdn_ssm_prefill or
+ * gdn_matmul_fp8 call made by this thread gives each wait between the warps of
+ * its kernels (gdn_prefill: of its chunked kernel) `cycles` SM cycles instead of the default of 2e9 (about one second), so that a test can
  * make a wait run out and check the abort path and gdn_prefill_status.  The
  * waits that let a kernel's own in-flight copies and tensor-core work finish
  * before it exits keep the default.  cycles = 0 disarms.  Returns
@@ -545,7 +545,8 @@ GDN_API gdn_status gdn_prefill_noalloc_status(uint32_t *detail, void *stream);
 
 /*
  * Timing hook for benchmarks.  Arms a one-shot on the calling host thread:
- * the next gdn_prefill or gdn_decode call made by this thread records
+ * the next gdn_prefill or gdn_decode call (gdn_kda_*, gdn_ssm_* likewise) made
+ * by this thread records
  * `begin_event` on its stream immediately before launching its main kernel
  * (the recurrence) and `end_event` immediately after it, so that
  * cudaEventElapsedTime gives that kernel's device time alone.  Both are

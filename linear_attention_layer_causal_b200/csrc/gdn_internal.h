@@ -153,6 +153,7 @@ struct SsmArgs {
     void *conv_cache = nullptr;  // decode: resident windows
     const float *conv_w, *conv_b, *A_log, *dt_bias, *D;
     void *ws = nullptr;
+    long long wait_limit = 0;    // prefill: SM cycles a wait between warps may take before the call aborts
     int segments = 1, fine = 1;  // prefill: segments per sequence, parts of each in the summary pass
     constexpr int conv_dim() const { return H * P + 2 * G * S; }
 };
@@ -184,6 +185,7 @@ struct MatmulArgs {
     int64_t out_stride;
     bool out_bf16;
     void *ws;
+    long long wait_limit; // SM cycles a wait between warps may take before the call aborts
 };
 size_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_matmul(const MatmulArgs &p, cudaStream_t s);

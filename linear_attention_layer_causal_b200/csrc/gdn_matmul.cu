@@ -88,10 +88,18 @@ constexpr int kScaleSlots = 4;
 struct Waiter {
     volatile uint32_t *abort_flag;
     uint32_t *status;
+    long long limit;
+    // A bound that was armed may be shorter than the sleep of a try_wait.
+    __device__ bool polled(uint32_t bar, uint32_t parity) const {
+        for (const long long t0 = clock64(); clock64() - t0 <= limit;)
+            if (mbar_test_wait(bar, parity))
+                return true;
+        return false;
+    }
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-        if (mbar_try_wait_spin(bar, parity))
+        if (mbar_test_wait(bar, parity))
             return true;
-        if (!*abort_flag && mbar_wait_bounded(bar, parity, kDefaultWaitLimit))
+        if (!*abort_flag && (limit >= kDefaultWaitLimit ? mbar_wait_bounded(bar, parity, limit) : polled(bar, parity)))
             return true;
         *abort_flag = 1;
         atomicOr(status, kStatusTimeout);
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                    sfull = tempty + 16, sempty = sfull + 8 * kScaleSlots;
     const int64_t tiles = (int64_t)tiles_m * tiles_n;
     const int KB = (int)((p.K + kBK - 1) / kBK);
-    const Waiter wait{&abort_flag, status};
+    const Waiter wait{&abort_flag, status, p.wait_limit};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -453,7 +461,7 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
     const int kb0 = KB * part / ks, kb1 = KB * (part + 1) / ks;
     const int tile = blockIdx.x / ks, tm = tile / tiles_n, tn = tile % tiles_n;
     const int64_t m0 = (int64_t)tm * BN, n0 = (int64_t)tn * 128;
-    const Waiter wait{&abort_flag, status};
+    const Waiter wait{&abort_flag, status, p.wait_limit};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(full + 8 * i, 1);

@@ -138,6 +138,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *para
     p.final_state = final_state;
     p.final_conv = final_conv;
     p.ws = workspace;
+    p.wait_limit = take_wait_limit();
     ssm_cut(cfg, batch, total_tokens, &p.segments, &p.fine);
     return cuda_status(launch_ssm_prefill(p, hook.begin, hook.end, (cudaStream_t)stream));
 }
@@ -240,7 +241,7 @@ gdn_status gdn_matmul_fp8(const void *a, const float *a_scale, const void *w, co
     const size_t need = matmul_workspace_bytes(M, N, K);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
         return GDN_ERR_WORKSPACE;
-    MatmulArgs p{a, w, a_scale, w_scale, M, N, K, out, out_stride, out_dtype == GDN_BF16, workspace};
+    MatmulArgs p{a, w, a_scale, w_scale, M, N, K, out, out_stride, out_dtype == GDN_BF16, workspace, take_wait_limit()};
     return cuda_status(launch_matmul(p, (cudaStream_t)stream));
 }
 

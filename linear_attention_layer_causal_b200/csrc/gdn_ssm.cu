@@ -18,9 +18,9 @@
 // With few sequences each is cut into segments, and a first run of the scan
 // kernel, without outputs, finds what each segment adds to the state.
 //
-// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 199 us (prep
-// 28, summary about 26, output pass 145), where moving the bytes would take 35 and
-// the MMAs 50.  What bounds it is the 16 warps' instructions: about 8000 cycles
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 198 us (prep
+// 28, summary about 26, output pass 145), where moving the bytes would take 35
+// and the MMAs 50.  What bounds it is the 16 warps' instructions: about 8000 cycles
 // a chunk (21000 instructions on 4 schedulers: the splits, the convolution, two
 // SiLUs), of which the tensor core is busy 2300.
 //
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     // 15.6).  A summary pass does not let the output pass set up beside it: a long document took 378 us for 350.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    // A wait that runs out (about a second) makes every role stop at its next
+    // A wait that runs out (about a second, unless the caller armed less) makes every role stop at its next
     // wait; what is in flight is waited for before the block ends.
     auto wait = [&](int i, uint32_t parity, bool patient = false) {
         bool ok = mbar_test_wait(bar(i), parity);
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             ok = mbar_test_wait(bar(i), parity);
         }
         if (!ok)
-            ok = !*abort_v && mbar_wait_sleeping(bar(i), parity, kDefaultWaitLimit);
+            ok = !*abort_v && mbar_wait_sleeping(bar(i), parity, p.wait_limit);
         if (!ok) {
             *abort_v = 1;
             atomicOr(a.status, kStatusTimeout);

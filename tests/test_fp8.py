@@ -347,3 +347,18 @@ def test_two_streams_and_status_words(M):
     ws = torch.full((gdn.matmul_fp8_workspace_size(M, 1000, 2048),), 255, dtype=torch.uint8, device="cuda")
     assert torch.equal(gdn.matmul_fp8(a, sa, w, sw, workspace=ws), want)
     assert (ws[:8] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 8192, 8192), (100, 4096, 4096), (3000, 4096, 4096)])
+def test_a_wait_that_runs_out_is_reported(M, N, K):
+    """With a bound of a few cycles on the waits between warps the call ends, says so, and the next one is whole."""
+    a, sa, w, sw = operands(M, N, K, 64)
+    ws = torch.empty(gdn.matmul_fp8_workspace_size(M, N, K), dtype=torch.uint8, device="cuda")
+    want = gdn.matmul_fp8(a, sa, w, sw, workspace=ws)
+    assert gdn.prefill_status(ws) == (gdn.GDN_OK, 0)
+    gdn.wait_limit_next_call(1)
+    gdn.matmul_fp8(a, sa, w, sw, workspace=ws)
+    assert gdn.prefill_status(ws)[0] == gdn.GDN_ERR_TIMEOUT
+    assert torch.equal(gdn.matmul_fp8(a, sa, w, sw, workspace=ws), want)
+    assert gdn.prefill_status(ws) == (gdn.GDN_OK, 0)

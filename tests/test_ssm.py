@@ -541,3 +541,21 @@ def test_segments_of_every_layout(dtype, S, P, segments):
     cfg = gdn.SsmConfig(2, 6, P, S, act_dtype=dtype, segments=segments)
     d, cu = make(cfg, lens, 30 + segments, wide=True)
     check(cfg, d, lens, prefill(cfg, d, cu, return_final_state=True, return_final_conv=True))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("segments", [1, 2])
+def test_a_wait_that_runs_out_is_reported(segments):
+    """With a bound of a few cycles on the waits between warps the call ends, says so, and the next one is whole."""
+    cfg = gdn.SsmConfig(1, 2, 64, 64, act_dtype="f32", segments=segments)
+    lens = [2000]
+    d, cu = make(cfg, lens, 24)
+    ws = torch.empty(gdn.ssm_prefill_workspace_size(cfg, 1, 2000), dtype=torch.uint8, device="cuda")
+    clean = prefill(cfg, d, cu, workspace=ws, return_final_state=True)
+    assert gdn.prefill_status(ws) == (gdn.GDN_OK, 0)
+    gdn.wait_limit_next_call(100)
+    prefill(cfg, d, cu, workspace=ws)
+    assert gdn.prefill_status(ws)[0] == gdn.GDN_ERR_TIMEOUT
+    again = prefill(cfg, d, cu, workspace=ws, return_final_state=True)
+    assert gdn.prefill_status(ws) == (gdn.GDN_OK, 0)
+    assert torch.equal(again["y"], clean["y"]) and torch.equal(again["final_state"], clean["final_state"])
