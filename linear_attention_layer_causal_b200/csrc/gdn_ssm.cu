@@ -18,7 +18,7 @@
 // With few sequences each is cut into segments, and a first run of the scan
 // kernel, without outputs, finds what each segment adds to the state.
 //
-// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 198 us (prep
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 197 us (prep
 // 28, summary about 26, output pass 145), where moving the bytes would take 35
 // and the MMAs 50.  What bounds it is the 16 warps' instructions: about 8000 cycles
 // a chunk (21000 instructions on 4 schedulers: the splits, the convolution, two
@@ -663,6 +663,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 mma_commit_if(bar(kBcEmpty + slot), issue);
                 next_slot();
             }
+            // (The loops over kk are not unrolled here: the 16 working warps fill the instruction caches, and a
+            // long document took 349 us for 344.)
             for (int c = 0; !SUMMARY && c < u.nc; ++c) {
                 const uint32_t ph = c & 1;
                 ok = wait_all(kBcFull + slot, sph) && wait_all(kHFull, ph);
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 // Y: D[row][t] = sum_s H[row][s] C[t][s].  H hi of 16 columns kk sits beside lo in the
                 // quarter of DH that its warpgroup owns.
                 const uint32_t ch = base + slot * K::kHalf, cl = ch + S * 128, yi = tmem + (ph ? K::kYI2 : K::kYI);
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < S / 16; ++kk) {
                     const uint32_t hh = tmem + K::kDH + kk / (CW / 16) * CW + kk % (CW / 16) * 8, hlo = hh + CW / 2;
                     const uint32_t off = kk / 4 * 8192 + kk % 4 * 32;
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 tc_fence_after();
                 // U: D[row][s] = sum_t x'[row][t] B[t][s], over H once the MMAs above have read it
                 const uint32_t bh = base + slot * K::kHalf, bl = bh + S * 128;
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < kQ / 16; ++kk) {
                     const uint32_t xh = tmem + K::kXP + 8 * kk, xl = xh + 32;
                     mma_bf16_ts_if(tmem + K::kDH, xh, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), kk > 0, issue);
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 // The masks are whole, with zeros above the diagonal: leaving the 16-blocks of zeros out by
                 // smaller MMAs took 3000 cycles instead of 768 (each then waits for the one before it).
                 const uint32_t mh = base + K::kOffM + mb * K::kMBytes, ml = mh + NH * kQ * kQ * 2;
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < kQ / 16; ++kk) {
                     const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
                     mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), kk > 0, issue);
@@ -732,7 +734,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 const uint32_t mbuf = base + K::kOffM + mb * K::kMBytes;
                 // 16-blocks (row, column): (0, 0) (3, 0) (3, 1) (3, 2) (3, 3) of one warp, (1, 0) (1, 1) (2, 0)
                 // (2, 1) (2, 2) of the other
-#pragma unroll 1
+#pragma unroll 1 // (unrolled: 223 us for 197 at 4096 tokens, for the same reason)
                 for (int blk = 0; blk < 5; ++blk) {
                     const int rb = warp == 2 ? (blk == 0 ? 0 : 3) : (blk < 2 ? 1 : 2);
                     const int i = warp == 2 ? (blk == 0 ? 0 : blk - 1) : (blk < 2 ? blk : blk - 2);
