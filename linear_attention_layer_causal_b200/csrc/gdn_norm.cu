@@ -57,14 +57,31 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// The outputs of unit u (active), and its share of the block's maximum.  The
-// maximum is taken over the bit patterns of |v|, which order like the values
-// and put infinity and NaN above all of them, so that neither is lost.
+// v / scale as e4m3 rounds the float32 quotient.  The product with the
+// reciprocal alone is off by up to 1.5 units and misses ties; one step with the
+// remainder, which a fused multiply-add has exactly (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990), leaves
+// about 2^-46 of the quotient before its rounding, and no such error reaches
+// across a tie or the middle between a tie and the float32 next to it
+// (tests/test_fp8_rounding.py goes through the quotients that come nearest).
+// The remainder's sign is chosen so that -0 stays -0.
+__device__ __forceinline__ void divide(float (&v)[8], float scale) {
+    const float inv = 1.0f / scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = v[i] * inv;
+        v[i] = fmaf(-fmaf(q, scale, -v[i]), inv, q);
+    }
+}
+
+// One unit, at element `at`: r and v are written out where they are asked for, v
+// stays.  Returns the unit's share of its block's maximum, which is taken over
+// the bit patterns of |v|: they order like the values and put infinity and NaN
+// above all of them, so that neither is lost.
 template <typename T>
-__device__ __forceinline__ void emit_unit(const NormArgs &p, bool active, int64_t row, int first, int u,
-                                          float rs, const Raw8<float> &w, float (&v)[8]) {
-    const int col = first + 8 * u; // column in the whole row
-    const int64_t at = row * p.dim + col;
+__device__ __forceinline__ uint32_t norm_unit(const NormArgs &p, bool active, int64_t at, float rs, const Raw8<float> &w,
+                                              float (&v)[8]) {
+    uint32_t m = 0u;
     if (active) {
         if (p.residual_out != nullptr)
             store8(reinterpret_cast<T *>(p.residual_out) + at, v);
@@ -75,30 +92,73 @@ __device__ __forceinline__ void emit_unit(const NormArgs &p, bool active, int64_
         }
         if (p.y != nullptr)
             store8(reinterpret_cast<T *>(p.y) + at, v);
-    }
-    if (p.q == nullptr)
-        return;
-    uint32_t m = 0u;
-    if (active) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
     }
+    return m;
+}
+// The maximum over the 16 lanes that hold a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
         m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (!active)
-        return;
+    return m;
+}
+// A block below 2^-71 (its remainders could be subnormal), or with an infinity or a NaN.
+__device__ __forceinline__ bool unusual(uint32_t m) { return m < 0x1c000000u || m >= 0x7f800000u; }
+
+// The 8-bit values of one unit, and its block's scale.
+template <bool DIVIDE>
+__device__ __forceinline__ void quant_unit(const NormArgs &p, int64_t row, int col, uint32_t m, float (&v)[8]) {
     const float amax = __uint_as_float(m);
     // fmaxf would drop a NaN maximum
     const float scale = m > 0x7f800000u ? amax : fmaxf(amax / 448.0f, 1.17549435e-38f);
-    const float inv = 1.0f / scale;
+    if (DIVIDE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = v[i] / scale;
+    } else {
+        divide(v, scale);
+    }
     uint2 b;
-    b.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
-    b.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
-    *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(p.q) + at) = b;
+    b.x = e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16);
+    b.y = e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16);
+    *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(p.q) + row * p.dim + col) = b;
     if ((col & 127) == 0)
         p.scale[row * ((p.dim + 127) / 128) + col / 128] = scale;
+}
+
+// The outputs of R units of a part, TPR apart from u on.  The units go through
+// each step together, with one choice between the two quotients for a warp's
+// units (4096 x 8192 bf16 with a residual: 40.9 us; unit by unit, each with its
+// own choice, 47.2; every quotient divided 60.8).
+template <typename T, int TPR, int R>
+__device__ __forceinline__ void emit(const NormArgs &p, int64_t row, int first, int u, int units, float rs,
+                                     const Raw8<float> (&w)[R], float (&v)[R][8]) {
+    uint32_t m[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        m[i] = norm_unit<T>(p, u + i * TPR < units, row * p.dim + first + 8 * (u + i * TPR), rs, w[i], v[i]);
+    if (p.q == nullptr)
+        return;
+    bool divided = false;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        m[i] = block_max(m[i]);
+        divided |= u + i * TPR < units && unusual(m[i]);
+    }
+    if (!__any_sync(0xffffffffu, divided)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (u + i * TPR < units)
+                quant_unit<false>(p, row, first + 8 * (u + i * TPR), m[i], v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (u + i * TPR < units)
+                quant_unit<true>(p, row, first + 8 * (u + i * TPR), m[i], v[i]);
+    }
 }
 
 // Row parts (norm groups) per `TPR` threads, NU units per thread in registers;
@@ -106,7 +166,7 @@ __device__ __forceinline__ void emit_unit(const NormArgs &p, bool active, int64_
 // With fewer blocks than parts a block takes every gridDim-th part: its
 // weights stay in registers (the host makes the step a multiple of the number
 // of groups), and the next part is on its way while this one is worked on.
-// 4096 x 8192 bf16 with a residual: 43.5 us, 5.4 TB/s; a block per row took 59.
+// 4096 x 8192 bf16 with a residual: 40.9 us, 5.8 TB/s; a block per row took 59.
 // One row of 8192: 3.4 us, its launch and a chain of load, two sums and store.
 template <typename T, int TPR, int NU>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T) == 2 ? 2 : 1) norm_kernel(const NormArgs p) {
@@ -193,17 +253,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T)
             rs = rsqrtf(ss / (float)len + p.eps);
         }
         if (NU > 0) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                if (TPR == 32 ? i * 32 < units : i * TPR + (tid & ~31) < units) // uniform over the warp
-                    emit_unit<T>(p, tid + i * TPR < units, row, first, tid + i * TPR, rs, w[i], v[i]);
-            }
+            emit<T, TPR, R>(p, row, first, tid, units, rs, w, v);
         } else {
             for (int u = tid; (u & ~31) < units; u += TPR) {
                 load(part, u);
                 load_w(u);
                 widen();
-                emit_unit<T>(p, u < units, row, first, u, rs, w[0], v[0]);
+                emit<T, TPR, R>(p, row, first, u, units, rs, w, v);
             }
         }
     }
