@@ -161,16 +161,25 @@ __device__ __forceinline__ void emit(const NormArgs &p, int64_t row, int first, 
     }
 }
 
+// Blocks of an instance that an SM holds at once: the launch bounds give each
+// the registers that this leaves it, and the host starts as many as run at once
+// (8192 x 2048 bf16 with a residual 26.8 us, and 35.2 where the registers left
+// room for three blocks of the four; 4096 x 2048 float32 19.5 with three, and
+// 24.4 with a grid for four).
+template <typename T, int TPR, int NU> constexpr int kResident =
+    TPR > 256 ? 1 : sizeof(T) == 2 ? (NU == 1 ? 4 : 2) : NU == 1 ? 3 : NU == 2 ? 2 : 1;
+
 // Row parts (norm groups) per `TPR` threads, NU units per thread in registers;
-// NU = 0: parts of any length, read a second time for the output.
+// NU = 0: parts of any length, two units at a time, read a second time for the
+// output (4096 x 16384 bf16 quantised: 90.9 us; with one unit at a time 116).
 // With fewer blocks than parts a block takes every gridDim-th part: its
 // weights stay in registers (the host makes the step a multiple of the number
 // of groups), and the next part is on its way while this one is worked on.
 // 4096 x 8192 bf16 with a residual: 40.9 us, 5.8 TB/s; a block per row took 59.
 // One row of 8192: 3.4 us, its launch and a chain of load, two sums and store.
 template <typename T, int TPR, int NU>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T) == 2 ? 2 : 1) norm_kernel(const NormArgs p) {
-    constexpr int kThreads = TPR < 256 ? 256 : TPR, R = NU > 0 ? NU : 1;
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, kResident<T, TPR, NU>) norm_kernel(const NormArgs p) {
+    constexpr int kThreads = TPR < 256 ? 256 : TPR, R = NU > 0 ? NU : 2;
     __shared__ float red[2][kThreads / 32];
     const int tid = threadIdx.x % TPR;
     const int64_t parts = p.rows * p.groups, step = (int64_t)gridDim.x * (kThreads / TPR);
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T)
                 load(part + step, tid);
             square(tid);
         } else if (has_norm) {
-            for (int u = tid; u < units; u += TPR) {
+            for (int u = tid; u < units; u += R * TPR) {
                 load(part, u);
                 widen();
                 square(u);
@@ -255,7 +264,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 && sizeof(T)
         if (NU > 0) {
             emit<T, TPR, R>(p, row, first, tid, units, rs, w, v);
         } else {
-            for (int u = tid; (u & ~31) < units; u += TPR) {
+            for (int u = tid; (u & ~31) < units; u += R * TPR) {
                 load(part, u);
                 load_w(u);
                 widen();
@@ -269,8 +278,7 @@ template <typename T, int TPR, int NU> cudaError_t go(const NormArgs &p, cudaStr
     constexpr int kThreads = TPR < 256 ? 256 : TPR, PER = kThreads / TPR;
     const int64_t parts = p.rows * p.groups, all = (parts + PER - 1) / PER;
     int64_t blocks = all;
-    // blocks that run at once: two to an SM, more where their registers are few
-    const int64_t at_once = (int64_t)148 * (NU == 1 ? 4 : 2);
+    const int64_t at_once = (int64_t)148 * kResident<T, TPR, NU>; // blocks that run at once
     if (NU > 0 && all > 3 * at_once && at_once >= p.groups)
         blocks = at_once / p.groups * p.groups; // the step is a multiple of the groups
     norm_kernel<T, TPR, NU><<<(unsigned)blocks, kThreads, 0, s>>>(p);
@@ -290,8 +298,8 @@ template <typename T> cudaError_t launch_t(const NormArgs &p, cudaStream_t s) {
         return go<T, 256, 1>(p, s);
     if (units <= 512)
         return go<T, 256, 2>(p, s);
-    if (units <= 1024)
-        return go<T, 256, 4>(p, s);
+    if (units <= 1024) // float32: two units a thread leave room for 16 warps (4096 x 8192: 73.6 us; four units, 80.4)
+        return sizeof(T) == 2 ? go<T, 256, 4>(p, s) : go<T, 512, 2>(p, s);
     return go<T, 256, 0>(p, s);
 }
 

@@ -156,3 +156,24 @@ def test_quantised_bits_of_tiny_and_huge_blocks_and_zeros(dim):
     assert v.isfinite().all() and float(v.abs().max()) > 1e33 and 0 < float(v[1].abs().max()) < 1e-33
     q, scale = gdn.quantize_fp8(v.cuda())
     same_bits(q, scale, v)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,dim,groups,dtype", [(700, 8192, 1, torch.float32), (1200, 8192, 2, torch.float32), (2000, 2048, 1, torch.float32),
+                                                   (3000, 2048, 1, torch.bfloat16), (500, 16392, 1, torch.bfloat16), (40, 24576, 1, torch.float32)])
+def test_many_rows_give_what_each_gives_alone(rows, dim, groups, dtype):
+    """Blocks that take several rows, and parts that are read twice, against the rows one by one."""
+    g = torch.Generator().manual_seed(dim)
+    x, r = (torch.randn(rows, dim, generator=g).cuda().to(dtype) for _ in range(2))
+    w = torch.randn(dim, generator=g).cuda()
+    out = gdn.rmsnorm_fp8(x, w, residual=r, groups=groups, return_y=True)
+    r2 = r.clone()
+    gdn.rmsnorm_fp8(x, w, residual=r2, groups=groups, residual_out=r2)
+    assert torch.equal(r2, out["residual"]) and torch.equal(r2, (x.float() + r.float()).to(dtype))
+    for i in (0, 1, rows // 2, rows - 1):
+        one = gdn.rmsnorm_fp8(x[i:i + 1], w, residual=r[i:i + 1], groups=groups, return_y=True)
+        near = (one["y"].double() - out["y"][i:i + 1].double()).abs() <= (torch.finfo(dtype).eps + 2.0 ** -20) * out["y"][i:i + 1].double().abs()
+        assert near.all()  # (a row alone may run with more threads, which sum its squares in another order)
+        assert torch.equal(one["residual"], out["residual"][i:i + 1])
+    if dtype == torch.float32:
+        same_bits(out["q"], out["scale"], out["y"])
