@@ -83,8 +83,10 @@ __device__ __forceinline__ void st_dsmem(uint32_t addr, unsigned long long x, un
 constexpr int kScaleSlots = 4;
 
 // Barriers and roles shared by the two kernels.  A wait that runs out (about a
-// second) makes every role stop at its next wait; what is in flight is waited
-// for before the block ends, and the status word says so.
+// second) makes every role stop at its next wait, and the status word says so.
+// Whichever role it was, what is in flight is waited for before the block ends:
+// the loading thread waits for its copies on every path, because a role that
+// gave up has not.
 struct Waiter {
     volatile uint32_t *abort_flag;
     uint32_t *status;
@@ -143,7 +145,7 @@ __device__ __forceinline__ bool load_blocks(const Waiter &wait, Ring<ST> &r, int
     return true;
 }
 
-// After a failed wait: the copies in flight land before the block may end.
+// After the last load, or a failed wait: the copies in flight land before the block may end.
 template <int ST> __device__ __forceinline__ void drain_loads(Ring<ST> r, int issued, uint32_t full) {
     for (int i = 0; i < issued; ++i) {
         r.back();
@@ -319,8 +321,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 tile_of(t, tiles_m, tiles_n, tm, tn);
                 ok = load_blocks<ST, 128, BN>(wait, r, issued, base, full, empty, &ta, &tw, tm * 128, tn * BN, 0, KB);
             }
-            if (!ok)
-                drain_loads(r, issued, full);
+            drain_loads(r, issued, full);
         } else if (warp == 1) {
             const uint32_t issue = elect_one();
             Ring<ST> r;
@@ -491,8 +492,8 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
         if (lane == 0) {
             Ring<ST> r;
             int issued = 0;
-            if (!load_blocks<ST, BN, 128>(wait, r, issued, base, full, empty, &ta, &tw, (int)m0, (int)n0, kb0, kb1))
-                drain_loads(r, issued, full);
+            load_blocks<ST, BN, 128>(wait, r, issued, base, full, empty, &ta, &tw, (int)m0, (int)n0, kb0, kb1);
+            drain_loads(r, issued, full);
         }
     } else if (warp == 1) {
         const uint32_t issue = elect_one();
