@@ -85,8 +85,8 @@ constexpr int kScaleSlots = 4;
 // Barriers and roles shared by the two kernels.  A wait that runs out (about a
 // second) makes every role stop at its next wait, and the status word says so.
 // Whichever role it was, what is in flight is waited for before the block ends:
-// the loading thread waits for its copies on every path, because a role that
-// gave up has not.
+// the loading thread waits for its copies and the MMA warp for its MMAs on
+// every path, because a role that gave up has not.
 struct Waiter {
     volatile uint32_t *abort_flag;
     uint32_t *status;
@@ -212,10 +212,13 @@ __device__ __forceinline__ bool issue_blocks(const Waiter &wait, Ring<ST> &r, Ri
     return true;
 }
 
-// After a failed wait: the MMAs in flight end before their memory is given back.
-template <int NB> __device__ __forceinline__ void drain_mma(const Ring<NB> &d, uint32_t tfull, uint32_t issue) {
-    mma_commit_if(tfull + 8 * d.i, issue);
-    mbar_wait_bounded(tfull + 8 * d.i, d.ph, kDefaultWaitLimit);
+// After the last MMA, or a failed wait: the MMAs in flight end before their
+// memory is given back.  A barrier of its own, used once: an accumulator's may
+// still be in the phase before the one that would be asked for, which a test of
+// its parity takes for the phase's end.
+__device__ __forceinline__ void drain_mma(uint32_t drain, uint32_t issue) {
+    mma_commit_if(drain, issue);
+    mbar_wait_bounded(drain, 0, kDefaultWaitLimit);
 }
 
 // 64 columns of one row from registers to out.
@@ -275,13 +278,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 int tiles_m, int tiles_n, uint32_t *status) {
     constexpr int ST = kWideStages, BN = kWideN;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * ST + 4 + 2 * kScaleSlots];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 4 + 2 * kScaleSlots + 1];
     __shared__ float scales[kScaleSlots * 4 * 128];
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * ST, tfull = empty + 8 * ST, tempty = tfull + 16,
-                   sfull = tempty + 16, sempty = sfull + 8 * kScaleSlots;
+                   sfull = tempty + 16, sempty = sfull + 8 * kScaleSlots, drain = sempty + 8 * kScaleSlots;
     const int64_t tiles = (int64_t)tiles_m * tiles_n;
     const int KB = (int)((p.K + kBK - 1) / kBK);
     const Waiter wait{&abort_flag, status, p.wait_limit};
@@ -298,6 +301,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             mbar_init(sfull + 8 * i, 2);
             mbar_init(sempty + 8 * i, 16);
         }
+        mbar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (blockIdx.x == 0)
@@ -328,8 +332,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             Ring<2> d;
             for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x)
                 ok = issue_blocks<ST, 2, 128, BN, BN, false>(wait, r, d, base, full, empty, tfull, tempty, tmem, KB, issue);
-            if (!ok)
-                drain_mma(d, tfull, issue);
+            drain_mma(drain, issue);
         } else if (warp >= 2) {
             Ring<kScaleSlots> r;
             for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -449,14 +452,14 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
     using T = Thin<BN>;
     constexpr int ST = T::kStages, NB = T::kBuffers, COLS = BN / T::kGroups, LD = COLS < 32 ? COLS : 32;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * ST + 2 * NB + 2 * kScaleSlots];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 2 * NB + 2 * kScaleSlots + 1];
     __shared__ __align__(16) float scales[kScaleSlots * 4 * BN];
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     float *join = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * ST, tfull = empty + 8 * ST, tempty = tfull + 8 * NB,
-                   sfull = tempty + 8 * NB, sempty = sfull + 8 * kScaleSlots;
+                   sfull = tempty + 8 * NB, sempty = sfull + 8 * kScaleSlots, drain = sempty + 8 * kScaleSlots;
     const int KB = (int)((p.K + kBK - 1) / kBK);
     const int part = ks > 1 ? (int)cluster_rank() : 0;
     const int kb0 = KB * part / ks, kb1 = KB * (part + 1) / ks;
@@ -476,6 +479,7 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
             mbar_init(sfull + 8 * i, 2);
             mbar_init(sempty + 8 * i, 4 * T::kGroups);
         }
+        mbar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (blockIdx.x == 0)
@@ -499,8 +503,8 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
         const uint32_t issue = elect_one();
         Ring<ST> r;
         Ring<NB> d;
-        if (!issue_blocks<ST, NB, BN, 128, BN, true>(wait, r, d, base, full, empty, tfull, tempty, tmem, kb1 - kb0, issue))
-            drain_mma(d, tfull, issue);
+        issue_blocks<ST, NB, BN, 128, BN, true>(wait, r, d, base, full, empty, tfull, tempty, tmem, kb1 - kb0, issue);
+        drain_mma(drain, issue);
     } else if (warp < 4) {
         Ring<kScaleSlots> r;
         load_scales<BN>(wait, r, scales, sfull, sempty, p.a_scale, m0, p.M, KB, p.w_scale + (int64_t)tn * KB, kb0, kb1,
@@ -569,6 +573,7 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
         } else {
             // each block of the cluster adds up its share of the rows: send it the sums, once the stages,
             // which hold them, are idle in all blocks
+            __syncwarp();
             cluster_sync();
             const int to = row * ks / 128, r0 = (128 * to + ks - 1) / ks;
             const uint32_t dst = mapa(smem_u32(join), to) + 4u * ((part * join_rows(ks) + row - r0) * (BN + 4) + COLS * wg);
