@@ -522,7 +522,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     // A wait that runs out (about a second, unless the caller armed less) makes every role stop at its next
-    // wait; what is in flight is waited for before the block ends.
+    // wait.  Whichever role it was, what is in flight is waited for before the block ends: the loading thread waits
+    // for its copies and the MMA warp for its MMAs on every path, because a role that gave up has not.
     auto wait = [&](int i, uint32_t parity, bool patient = false) {
         bool ok = mbar_test_wait(bar(i), parity);
         // the loads and M run ahead: they ask now and then, and leave the schedulers to the others
@@ -578,6 +579,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 // In the order in which the room for them comes free: that of z of chunk c - 2 does before that of
                 // x of chunk c, and both before C B^T's and B's.  Rows of x before the sequence or behind it, and of z behind it, are another
                 // sequence's, or zeros; channels of absent heads are whatever lies there.  Neither is used.
+                // A worker that gave up gives its room back without having waited for what was on its way there: hence
+                // the look at the flag.
                 int cbs = 0, raws = 0, zs = 0; // loaded so far
                 bool ok = true;
                 for (int c = 0; ok && c < (SUMMARY ? u.nc : u.nc + 2); ++c) {
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     if (!SUMMARY && c < u.nc && !(ok = load_bc(y, 2 * S))) // C
                         break;
                     if (!SUMMARY && c >= 2 && p.z != nullptr) {
-                        if (!(ok = wait(kZEmpty, (c & 1) ^ 1)))
+                        if (!(ok = wait(kZEmpty, (c & 1) ^ 1) && !*abort_v))
                             break;
                         mbar_arrive_expect_tx(bar(kZFull), kQ * K::kRow);
                         tma_load_2d(base + K::kOffZ, &tz, u.h0 * P, (int)(tok0 + (int64_t)(c - 2) * kQ), bar(kZFull));
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     }
                     if (c < u.nc) {
                         const int rs = raw_slot(c);
-                        if (!(ok = wait(kRawEmpty + rs, raw_phase(c) ^ 1)))
+                        if (!(ok = wait(kRawEmpty + rs, raw_phase(c) ^ 1) && !*abort_v))
                             break;
                         // (x's room is free, so the weights of the chunk four before are done with too)
                         mbar_arrive_expect_tx(bar(kRawFull + rs), K::kXBytes + gbytes);
@@ -616,21 +619,21 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         ok = load_bc(y, 0); // B
                     }
                 }
-                if (!ok) { // gave up: the copies in flight land before the block may end
-                    for (int c = max(cbs - K::kCbBufs, 0); c < cbs; ++c)
-                        mbar_wait_bounded(bar(kCbFull + c % K::kCbBufs), (c / K::kCbBufs) & 1, kDefaultWaitLimit);
-                    if (zs > 0)
-                        mbar_wait_bounded(bar(kZFull), (zs - 1) & 1, kDefaultWaitLimit);
-                    for (int c = max(raws - 2, 0); c < raws; ++c)
-                        if (SUMMARY || c == raws - 1)
-                            mbar_wait_bounded(bar(kRawFull + raw_slot(c)), raw_phase(c), kDefaultWaitLimit);
-                    for (int k = 0; k < used; ++k) {
-                        if (--slot < 0) {
-                            slot = K::kSlots - 1;
-                            ph ^= 1;
-                        }
-                        mbar_wait_bounded(bar(kBcFull + slot), ph ^ 1, kDefaultWaitLimit);
+                // The copies in flight land: each buffer's last one, since its room was given back for it only
+                // after the one before had landed.
+                for (int c = max(cbs - K::kCbBufs, 0); c < cbs; ++c)
+                    mbar_wait_sleeping(bar(kCbFull + c % K::kCbBufs), (c / K::kCbBufs) & 1, kDefaultWaitLimit);
+                if (zs > 0)
+                    mbar_wait_sleeping(bar(kZFull), (zs - 1) & 1, kDefaultWaitLimit);
+                for (int c = max(raws - 2, 0); c < raws; ++c)
+                    if (SUMMARY || c == raws - 1)
+                        mbar_wait_sleeping(bar(kRawFull + raw_slot(c)), raw_phase(c), kDefaultWaitLimit);
+                for (int k = 0; k < used; ++k) {
+                    if (--slot < 0) {
+                        slot = K::kSlots - 1;
+                        ph ^= 1;
                     }
+                    mbar_wait_sleeping(bar(kBcFull + slot), ph ^ 1, kDefaultWaitLimit);
                 }
             }
         } else if (warp == 1) { // ---- MMAs
@@ -718,10 +721,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 }
                 mma_commit_if(bar(kIDone + (c & 1)), issue);
             }
-            if (!ok) { // the MMAs in flight end before their memory is given back
-                mma_commit_if(bar(kDrain), issue);
-                mbar_wait_bounded(bar(kDrain), 0, kDefaultWaitLimit);
-            }
+            // the MMAs in flight end before their memory is given back
+            mma_commit_if(bar(kDrain), issue);
+            mbar_wait_sleeping(bar(kDrain), 0, kDefaultWaitLimit);
         } else { // ---- M: the decay masks times C B^T, as operands; two warps
             const int odd = lane & 1; // a thread has a row and every other group of 8 columns
             const float D0 = p.D != nullptr ? -kLn2 * __ldg(p.D + u.h0) : 0.f;
@@ -814,7 +816,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             }
         };
         const int64_t gstate = (((int64_t)u.n * p.H + u.h0) * P + row) * S + CW * part;
-        bool ok = true; // when a wait gave up, the rest runs without waiting: the outputs are invalid anyway
+        // When a wait gave up, the rest runs without waiting: the outputs are invalid anyway.  (It still arrives at
+        // the barriers, with the flag set before: the loading thread looks at that before it loads over x or z.)
+        bool ok = true;
         // x of the chunk of tokens t0 .., the i-th that is loaded: tokens 16 part ..
         auto take_x = [&](int i, int64_t t0, float (&x)[16]) {
             const int rs = raw_slot(i);

@@ -54,3 +54,42 @@ def test_products_that_give_up(M, N, K):
             times += given_up(ws, g, want)
             assert torch.equal(s, want_small) and torch.equal(b, want)
     assert times > 0  # a bound of a cycle is below any copy's time
+
+
+def mixer(lens, P, S, dtype, segments, gate, seed):
+    cfg = gdn.SsmConfig(2, 6, P, S, act_dtype=dtype, segments=segments)
+    g = torch.Generator().manual_seed(seed)
+    act = torch.bfloat16 if dtype == "bf16" else torch.float32
+    N, B, C = sum(lens), len(lens), cfg.conv_dim
+    cu = torch.tensor([sum(lens[:i]) for i in range(B + 1)], dtype=torch.int32, device="cuda")
+    xbc, dt, z = (torch.randn(*s, generator=g).cuda().to(act) for s in ((N, C), (N, 6), (N, 6, P)))
+    kw = dict(conv_b=0.1 * torch.randn(C, generator=g).cuda(), dt_bias=torch.randn(6, generator=g).cuda() - 3,
+              D=torch.randn(6, generator=g).cuda(), z=z if gate else None,
+              initial_state=0.1 * torch.randn(B, 6, P, S, generator=g).cuda(), initial_conv=torch.randn(B, 3, C, generator=g).cuda().to(act))
+    conv_w, A_log = 0.5 * torch.randn(C, 4, generator=g).cuda(), torch.rand(6, generator=g).cuda()
+
+    def call(ws=None):
+        out = gdn.ssm_prefill(cfg, xbc, dt, cu, conv_w, A_log, return_final_state=True, workspace=ws, **kw)
+        return torch.cat([out["y"].float().flatten(), out["final_state"].flatten()])
+    return call, gdn.ssm_prefill_workspace_size(cfg, B, N)
+
+
+# one chunk (the loading warp never waits), a few, many, and sequences of both kinds in one batch
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,segments", [([37], 1), ([64, 1, 0], 1), ([200], 1), ([130, 20], 2), ([1500], 1), ([1500, 64], 5)])
+@pytest.mark.parametrize("P,S,dtype,gate", [(64, 64, "bf16", True), (64, 128, "f32", True), (128, 64, "bf16", False), (128, 128, "bf16", True)])
+def test_prompts_that_give_up(lens, segments, P, S, dtype, gate):
+    call, need = mixer(lens, P, S, dtype, segments, gate, 5)
+    small = operands(3, 520, 640, 2)
+    want, want_small = call(), gdn.matmul_fp8(*small)
+    times = 0
+    for limit in LIMITS:
+        wss, got, behind = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(3)], [], []
+        for ws in wss:
+            gdn.wait_limit_next_call(limit)
+            got.append(call(ws))
+            behind.append((gdn.matmul_fp8(*small), call()))
+        for ws, g, (s, b) in zip(wss, got, behind):
+            times += given_up(ws, g, want)
+            assert torch.equal(s, want_small) and torch.equal(b, want)
+    assert times > 0 or max(lens) <= 200  # its waits sleep some microseconds before they look at the bound
