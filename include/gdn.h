@@ -209,11 +209,14 @@ GDN_API gdn_status gdn_prefill_status(const void *workspace, size_t workspace_by
 /*
  * Testing hook for the bounded waits above.  Arms a one-shot on the calling
  * host thread: the next gdn_prefill, gdn_prefill_noalloc, gdn_ssm_prefill or
- * gdn_matmul_fp8 call made by this thread gives each wait between the warps of
- * its kernels (gdn_prefill: of its chunked kernel) `cycles` SM cycles instead of the default of 2e9 (about one second), so that a test can
- * make a wait run out and check the abort path and gdn_prefill_status.  The
- * waits that let a kernel's own in-flight copies and tensor-core work finish
- * before it exits keep the default.  cycles = 0 disarms.  Returns
+ * gdn_matmul_fp8 call that this thread makes with valid arguments, one without
+ * tokens or rows too, gives each wait between the warps of its kernels
+ * (gdn_prefill: of its chunked kernel) `cycles` SM cycles instead of the
+ * default of 2e9 (about one second), so that a test can make a wait run out and
+ * check the abort path and gdn_prefill_status.  A wait of gdn_ssm_prefill
+ * sleeps before it looks at the bound, 2 microseconds at a time and up to 3 at
+ * first.  The waits that let a kernel's own in-flight copies and tensor-core
+ * work finish before it exits keep the default.  cycles = 0 disarms.  Returns
  * GDN_ERR_INVALID_ARG for a negative value.
  */
 GDN_API gdn_status gdn_wait_limit_next_call(int64_t cycles);

@@ -258,8 +258,8 @@ def prefill_noalloc_status(stream=None) -> tuple[int, int]:
 
 
 def wait_limit_next_call(cycles: int) -> None:
-    """Testing hook: the next prefill call on this thread bounds each wait between
-    the warps of its chunked kernel by `cycles` SM cycles (0 = default, ~1 s)."""
+    """Testing hook: the next prefill, ssm_prefill or matmul_fp8 call on this thread bounds
+    each wait between the warps of its kernels by `cycles` SM cycles (0 = default, ~1 s)."""
     st = lib().gdn_wait_limit_next_call(int(cycles))
     if st != GDN_OK:
         raise GdnError(st, "gdn_wait_limit_next_call")

@@ -128,6 +128,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *para
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
         return GDN_ERR_WORKSPACE;
     const ProfileHook hook = take_profile_hook();
+    const long long wait_limit = take_wait_limit();
     if (batch == 0)
         return GDN_OK;
     SsmArgs p = ssm_args(cfg, params, xbc, xbc_stride, dt, dt_stride, z, z_stride, batch, y);
@@ -138,7 +139,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_params *para
     p.final_state = final_state;
     p.final_conv = final_conv;
     p.ws = workspace;
-    p.wait_limit = take_wait_limit();
+    p.wait_limit = wait_limit;
     ssm_cut(cfg, batch, total_tokens, &p.segments, &p.fine);
     return cuda_status(launch_ssm_prefill(p, hook.begin, hook.end, (cudaStream_t)stream));
 }
@@ -231,8 +232,10 @@ gdn_status gdn_matmul_fp8(const void *a, const float *a_scale, const void *w, co
         return st;
     if (!dtype_ok(out_dtype))
         return GDN_ERR_INVALID_ARG;
-    if (M == 0 || N == 0)
+    if (M == 0 || N == 0) {
+        take_wait_limit(); // the armed bound was for this call
         return GDN_OK;
+    }
     if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr ||
         out_stride < N || out_stride > INT32_MAX)
         return GDN_ERR_INVALID_ARG;

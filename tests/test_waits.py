@@ -93,3 +93,26 @@ def test_prompts_that_give_up(lens, segments, P, S, dtype, gate):
             times += given_up(ws, g, want)
             assert torch.equal(s, want_small) and torch.equal(b, want)
     assert times > 0 or max(lens) <= 200  # its waits sleep some microseconds before they look at the bound
+
+
+@pytest.mark.gpu
+def test_a_call_without_work_takes_the_armed_bound():
+    """The bound is for the next call, whatever that has to do: the one after it runs unbounded again."""
+    a, sa, w, sw = operands(100, 1000, 768, 1)
+    want, ws = gdn.matmul_fp8(a, sa, w, sw), workspace(100, 1000, 768)
+    call, need = mixer([1500], 64, 64, "bf16", 1, True, 5)
+    cfg = gdn.SsmConfig(2, 6, 64, 64)
+    none = torch.empty(0, cfg.conv_dim, dtype=torch.bfloat16, device="cuda")
+    want_y, ws_y = call(), torch.empty(need, dtype=torch.uint8, device="cuda")
+    empty = [lambda: gdn.matmul_fp8(a[:0], sa[:0], w, sw), lambda: gdn.matmul_fp8(a, sa, w[:0], sw[:0]),
+             lambda: gdn.ssm_prefill(cfg, none, none[:, :6], torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                     torch.zeros(cfg.conv_dim, 4, device="cuda"), torch.zeros(6, device="cuda"))]
+    for nothing in empty:
+        gdn.wait_limit_next_call(1)
+        nothing()
+        got = gdn.matmul_fp8(a, sa, w, sw, workspace=ws)
+        assert gdn.prefill_status(ws) == (gdn.GDN_OK, 0) and torch.equal(got, want)
+        gdn.wait_limit_next_call(1)
+        nothing()
+        got = call(ws_y)
+        assert gdn.prefill_status(ws_y) == (gdn.GDN_OK, 0) and torch.equal(got, want_y)
