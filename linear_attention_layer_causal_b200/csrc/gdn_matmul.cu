@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         mbar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (blockIdx.x == 0)
+        if (blockIdx.x == 0 && wait.limit >= kDefaultWaitLimit) // (see launch_matmul)
             status[0] = status[1] = 0;
     }
     if (warp == 1)
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(Thin<BN>::kThreads, 1)
         mbar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (blockIdx.x == 0)
+        if (blockIdx.x == 0 && wait.limit >= kDefaultWaitLimit) // (see launch_matmul)
             status[0] = status[1] = 0;
     }
     if (warp == 1)
@@ -710,7 +710,15 @@ template <typename O> cudaError_t launch_t(const MatmulArgs &p, cudaStream_t s) 
 // The first word of the workspace is the kernels' status word.
 size_t matmul_workspace_bytes(int64_t, int64_t, int64_t) { return kWorkspaceHeader; }
 
+// The status words are cleared by the first block, which starts first: long
+// before another one's wait of a second can run out.  An armed bound may run out
+// before that, and its report would be lost: there they are cleared ahead.
 cudaError_t launch_matmul(const MatmulArgs &p, cudaStream_t s) {
+    if (p.wait_limit < kDefaultWaitLimit) {
+        const cudaError_t e = cudaMemsetAsync(p.ws, 0, 2 * sizeof(uint32_t), s);
+        if (e != cudaSuccess)
+            return e;
+    }
     return p.out_bf16 ? launch_t<__nv_bfloat16>(p, s) : launch_t<float>(p, s);
 }
 

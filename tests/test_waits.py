@@ -116,3 +116,21 @@ def test_a_call_without_work_takes_the_armed_bound():
         nothing()
         got = call(ws_y)
         assert gdn.prefill_status(ws_y) == (gdn.GDN_OK, 0) and torch.equal(got, want_y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 300, 256), (16, 128, 1024), (1000, 4096, 256)])
+def test_every_call_that_gave_up_says_so(M, N, K):
+    """Many short calls with a bound of a cycle, each with status words that an earlier call left set: whatever
+    block's wait runs out first, a wrong result never comes with a clear status."""
+    a, sa, w, sw = operands(M, N, K, 3)
+    want = gdn.matmul_fp8(a, sa, w, sw)
+    words = torch.full((300, gdn.matmul_fp8_workspace_size(M, N, K)), 255, dtype=torch.uint8, device="cuda")
+    outs = []
+    for ws in words:
+        gdn.wait_limit_next_call(1)
+        outs.append(gdn.matmul_fp8(a, sa, w, sw, workspace=ws))
+    words = words[:, :8].contiguous().view(torch.int32).tolist()
+    for (status, detail), out in zip(words, outs):
+        assert status in (0, 1) and detail == 0
+        assert status == 1 or torch.equal(out, want)
