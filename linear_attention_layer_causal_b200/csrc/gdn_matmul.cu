@@ -11,6 +11,7 @@
 //     a cluster; for few rows of a, where reading w once is the bound.
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "gdn_per_device.h"
 #include "gdn_sm100.cuh"
 #include "gdn_tmap.h"
 
@@ -637,29 +638,39 @@ template <int BN, typename O> cudaLaunchConfig_t thin_config(unsigned blocks, in
 
 // Clusters of 1 .. 8 blocks that run at once, as the runtime counts them (the
 // SMs of a cluster are of one GPC, so 148 SMs hold fewer clusters of 8 than
-// 18).  Asked once per process; it decides a launch shape only.
-template <int BN, typename O> struct Capacity {
-    int clusters[9] = {};
-    cudaError_t error;
-    Capacity() {
-        error = cudaFuncSetAttribute(thin_kernel<BN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Thin<BN>::kSmem);
-        for (int ks = 1; ks <= 8 && error == cudaSuccess; ++ks) {
+// 18).  Asked once per device; it decides a launch shape only.
+struct Capacity {
+    int clusters[9];
+};
+template <int BN, typename O> cudaError_t thin_capacity(const Capacity **cap) {
+    static PerDevice<Capacity> known;
+    int device = -1;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess)
+        return e;
+    return known.get(device, [](Capacity *c) {
+        cudaError_t err = cudaFuncSetAttribute(thin_kernel<BN, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Thin<BN>::kSmem);
+        for (int ks = 1; ks <= 8 && err == cudaSuccess; ++ks) {
             cudaLaunchAttribute at{};
             const cudaLaunchConfig_t cfg = thin_config<BN, O>(400 * ks, ks, &at, nullptr);
-            error = cudaOccupancyMaxActiveClusters(&clusters[ks], thin_kernel<BN, O>, &cfg);
+            err = cudaOccupancyMaxActiveClusters(&c->clusters[ks], thin_kernel<BN, O>, &cfg);
         }
-    }
-};
+        return err;
+    }, cap);
+}
 
 // Blocks of a cluster for this many tiles and blocks of k: the most that still
 // all run at once, with two blocks of k each at least.
 template <int BN, typename O> cudaError_t thin_split(int64_t tiles, int KB, int *ks) {
-    static const Capacity<BN, O> cap;
+    const Capacity *cap = nullptr;
+    const cudaError_t e = thin_capacity<BN, O>(&cap);
+    if (e != cudaSuccess)
+        return e;
     *ks = 1;
     for (int k = 2; k <= 8 && 2 * k <= KB; ++k)
-        if (tiles <= cap.clusters[k])
+        if (tiles <= cap->clusters[k])
             *ks = k;
-    return cap.error;
+    return cudaSuccess;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
