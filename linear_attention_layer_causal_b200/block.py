@@ -19,7 +19,8 @@ from . import (BLOCK, Config, SsmConfig, decode, matmul_fp8, prefill, quantize_f
 
 
 def in_projection_rows(mixer: Union[Config, SsmConfig]) -> list:
-    """Rows of the in-projection's weight by part, each part's padded to whole blocks of 128.
+    """Rows of the in-projection's weight by part, each part's padded to whole blocks of 128 (what
+    the rows behind a part hold is not used).
 
     A state-space mixer reads its parts as slices of one product's rows, z | x|B|C | dt; Gated
     DeltaNet takes contiguous tensors, so that qkv, z and a|b are products of their own."""
@@ -28,8 +29,12 @@ def in_projection_rows(mixer: Union[Config, SsmConfig]) -> list:
     if isinstance(mixer, SsmConfig):
         hp = mixer.num_heads * mixer.head_dim
         return [("z|xbc|dt", pad(hp + mixer.conv_dim + mixer.num_heads))]
-    return [("qkv", mixer.conv_dim), ("z", mixer.num_v_heads * mixer.head_dim),
+    return [("qkv", pad(mixer.conv_dim)), ("z", pad(mixer.num_v_heads * mixer.head_dim)),
             ("a|b", pad(2 * mixer.num_v_heads))]
+
+
+def _heads(mixer):
+    return mixer.num_heads if isinstance(mixer, SsmConfig) else mixer.num_v_heads
 
 
 @dataclass
@@ -55,6 +60,15 @@ class MixerBlock:
         rows = sum(n for _, n in in_projection_rows(self.mixer))
         if self.in_w.shape[0] != rows:
             raise ValueError(f"in_w must have {rows} rows {in_projection_rows(self.mixer)}, got {self.in_w.shape[0]}")
+        hidden, width = self.in_w.shape[1], _heads(self.mixer) * self.mixer.head_dim
+        for name, shape in (("norm_w", (hidden,)), ("in_scale", (rows // BLOCK, -(-hidden // BLOCK))),
+                            ("out_w", (hidden, width)), ("out_scale", (-(-hidden // BLOCK), -(-width // BLOCK))),
+                            ("out_norm_w", (width,))):
+            t = getattr(self, name)
+            if t is None and name == "out_norm_w":
+                continue
+            if t is None or tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have the shape {shape}, got {None if t is None else tuple(t.shape)}")
 
     def _project(self, hidden, residual):
         n = rmsnorm_fp8(hidden, self.norm_w, residual=residual, eps=self.eps, weight_offset=self.weight_offset)
@@ -73,8 +87,8 @@ class MixerBlock:
                         dt=rows[:, hp + m.conv_dim:hp + m.conv_dim + m.num_heads])
         qkv, z, ab = parts
         h = m.num_v_heads
-        return dict(qkv=qkv, a=ab[:, :h].contiguous(), b=ab[:, h:2 * h].contiguous(),
-                    z=z.unflatten(1, (h, m.head_dim)))
+        return dict(qkv=qkv[:, :m.conv_dim].contiguous(), a=ab[:, :h].contiguous(), b=ab[:, h:2 * h].contiguous(),
+                    z=z[:, :h * m.head_dim].contiguous().unflatten(1, (h, m.head_dim)))
 
     def _out(self, y):
         flat = y.flatten(1)
