@@ -361,9 +361,11 @@ GDN_API gdn_status gdn_kda_decode(const gdn_config *cfg, const gdn_kda_params *p
  *     S_t = exp(-exp(A_log) delta) S_{t-1} + delta x_t B_t^T
  *     y_t = (S_t C_t + D x_t) * SiLU(z_t)
  * where head h reads B and C of group h / (H / G).  All arithmetic between the
- * inputs and y is carried in float32 (matrix products on the tensor cores take
- * each operand as a sum of two bfloat16 parts, three products each, which
- * keeps about 16 bits of every operand).
+ * inputs and y is carried in float32.  In prompts, matrix products on the tensor
+ * cores take each operand as a sum of two 16-bit parts, three products each: 22
+ * bits of every operand, except that with GDN_BF16 activations the read-out (H C
+ * and the products within a chunk, not the state) keeps about 16.  Operands of 22
+ * bits are held to 2^-39 of the chunk's largest (the row's, of x and H) at worst.
  *
  * Row strides: xbc, dt and z may be parts of wider rows (one in-projection's
  * output): the stride is in elements, at least the part's own length, and for

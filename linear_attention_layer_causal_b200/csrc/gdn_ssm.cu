@@ -18,18 +18,29 @@
 // With few sequences each is cut into segments, and a first run of the scan
 // kernel, without outputs, finds what each segment adds to the state.
 //
-// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 197 us (prep
-// 28, summary about 26, output pass 145), where moving the bytes would take 35
-// and the MMAs 50.  What bounds it is the 16 warps' instructions: about 8000 cycles
-// a chunk (21000 instructions on 4 schedulers: the splits, the convolution, two
-// SiLUs), of which the tensor core is busy 2300.
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 212 us (by
+// themselves: prep 31, summary 42, output pass 148), where moving the bytes would
+// take 35 and the MMAs 50.  What bounds it is the 16 warps' instructions and their
+// latency: two thirds of the issue slots, four such warps to a scheduler (the
+// splits, the convolution, two SiLUs); the tensor core is busy for a quarter.
 //
-// Precision: every operand of a product is the sum of two bfloat16 parts, each
-// product three MMAs (the product of the two second parts is left out): about
-// 2^-17 of each term, where single bfloat16 operands would put 2^-9 on the
-// float32 state.  Log-decays are summed in 64 bits and M takes their difference
-// as two floats: at G = -1000 one float's step alone is 6e-5.
+// Precision: every operand of a product is the sum of two 16-bit parts, each
+// product three MMAs (the product of the two second parts is left out).  x' and B,
+// which make the state, are float16 parts, 22 bits of each: the state that is left
+// is as exact as a float32 recurrence's (2e-7 against 64 bits, where bfloat16
+// parts left 4e-6 and took 197 us).  Where y is float32 so are all other operands;
+// where it is bfloat16 they are bfloat16 parts, 2^-17 of each term under y's own
+// 2^-9.  float16 has a narrow range, so its operands are scaled by powers of two:
+// B and C by their largest in the chunk, x and x' by the largest of each row (for
+// which the four threads of a row meet once a chunk), H by a bound of each row, M
+// by the largest product and step and by D.  A value of 2^-17 of that largest has
+// all its bits; what is smaller is held to 2^-39 of the largest (x' and B where
+// they only just make H up: 2^-29).
+// Log-decays are summed in 64 bits and M takes their difference as two floats: at
+// G = -1000 one float's step alone is 6e-5.  The SiLUs' and masks' exponentials
+// and reciprocals are the approximate ones, 2^-22 each.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_sm100.cuh"
 #include "gdn_ssm.cuh"
@@ -43,6 +54,7 @@ using namespace sm100;
 constexpr int kQ = 64;        // tokens of a chunk
 constexpr int kMaskRec = 192; // floats of a (chunk, head) for M: G / ln 2, its low part, -ln 2 delta
 constexpr int kGateRec = 128; // and for the rest: -ln 2 x' weight, e^G
+constexpr int kScaleRec = 4;  // floats of a (chunk, group): what B and C are to be multiplied with
 constexpr int kSMs = 148;
 constexpr uint32_t kStatusTimeout = 1u;
 
@@ -55,7 +67,7 @@ __device__ __forceinline__ int64_t first_chunk(int64_t start, int n) { return st
 int64_t max_chunks(int64_t N, int batch) { return N / kQ + batch; }
 
 struct Layout { // workspace offsets in bytes
-    size_t bc, cb, masks, gates, seg, segdecay, total;
+    size_t bc, cb, masks, gates, scales, seg, segdecay, total;
 };
 Layout layout(int G, int H, int P, int S, int64_t N, int batch, int slots) {
     const size_t chunks = (size_t)max_chunks(N, batch);
@@ -65,7 +77,8 @@ Layout layout(int G, int H, int P, int S, int64_t N, int batch, int slots) {
     l.cb = l.bc + round_up(chunks * G * kQ * 4 * S * 2);
     l.masks = l.cb + round_up(chunks * G * kQ * kQ * 4);
     l.gates = l.masks + round_up(chunks * H * kMaskRec * 4);
-    l.seg = l.gates + round_up(chunks * H * kGateRec * 4);
+    l.scales = l.gates + round_up(chunks * H * kGateRec * 4);
+    l.seg = l.scales + round_up(chunks * G * kScaleRec * 4);
     l.segdecay = l.seg + (slots > 1 ? round_up((size_t)batch * tiles * slots * 128 * S * 4) : 0);
     l.total = l.segdecay + (slots > 1 ? round_up((size_t)batch * tiles * slots * 2 * 4) : 0);
     return l;
@@ -99,12 +112,51 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// Two floats as bfloat16 parts: hi = the nearest, lo = what is left, each
-// packed with the first in the low half.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
-    const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb), "f"(ra));
+// Two floats as two 16-bit parts: hi = the nearest, lo = what is left, each
+// packed with the first in the low half.  F16: float16 (22 bits in all, within
+// its range), or bfloat16 (16 bits).
+template <bool F16> __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    float ha, hb;
+    if (F16) {
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+        asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(ha), "=f"(hb) : "r"(hi));
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b - hb), "f"(a - ha));
+    } else {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+        ha = __uint_as_float(hi << 16);
+        hb = __uint_as_float(hi & 0xffff0000u);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b - hb), "f"(a - ha));
+    }
+}
+
+// Scales.  A largest value with the exponent field e is brought to 2^13 .. 2^14
+// by up(e) and back by down(e); both are powers of two, down(e) = 1 / up(e), and
+// a field below 14 counts as 14 (values near the smallest normal float).
+__device__ __forceinline__ float up(int e) { return __int_as_float(min(267 - e, 253) << 23); }
+__device__ __forceinline__ float down(int e) { return __int_as_float(max(e - 13, 1) << 23); }
+__device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) & 0xff; }
+// The largest magnitude of three; NaN where one is (magnitude_nan), or left out.
+__device__ __forceinline__ float magnitude_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float magnitude(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// 2^n, n clamped to the normal floats.
+__device__ __forceinline__ float pow2(int n) { return __int_as_float((max(min(n, 127), -126) + 127) << 23); }
+// The larger of each half, and the largest of all four halves.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ int largest_half(uint32_t a, uint32_t b) {
+    const uint32_t m = max_halves(a, b);
+    return (int)max(m >> 16, m & 0xffffu);
 }
 
 // Two outputs to their rows in shared memory, one conversion for both.
@@ -129,6 +181,9 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// float32 outputs: every operand as float16 parts.  bfloat16 outputs: those of the state, x' and B, only.
+template <typename T> constexpr bool kWhole = sizeof(T) == 4;
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // SiLU(x) = x / (1 + 2^p), p = -x log2(e); also times y, for a pair.
@@ -176,21 +231,31 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// e^g to float32's precision: an exponent of -16 rounded to a float would leave 2^-21 of it.
+__device__ __forceinline__ float exp_of(double g) {
+    const float h = (float)g;
+    return expf(h) * (1.f + (float)(g - (double)h));
+}
+
 // One chunk and group; the blocks of z = 1 have the gates.  Writes, for the scan kernel: the rows [64][4 S] of
-// B hi | B lo | C hi | C lo (zero behind the sequence's end), the 64 x 64
-// products C_t . B_s of s's and t's 16-blocks with s <= t, and the records of
-// each head of the group.
+// B hi | B lo | C hi | C lo (zero behind the sequence's end), scaled; what B and C
+// were scaled back with; the 64 x 64 products C_t . B_s of the scaled ones, of
+// s's and t's 16-blocks with s <= t (where outputs are float32, in the place of
+// row 0, columns 16 to 18, also the two factors and the largest of them; else
+// scaled back); and the records of each head of the group.
 template <typename T, int S>
-__global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs p, __nv_bfloat16 *bc, float *cb, float *masks, float *gates,
+__global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs p, uint16_t *bc, float *cb, float *masks, float *gates, float *scales,
                                                                 uint32_t *status) {
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint32_t largest[2][kPrepThreads / 32];
+    __shared__ float back[2]; // what the scaled B and C are to be multiplied with
     constexpr int LDS = S + 8; // row length in shared memory: rows 16 bytes apart in banks
     const int64_t id = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -221,7 +286,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
         const int hpg = p.H / p.G;
         for (int k = warp; k < hpg; k += kPrepThreads / 32) {
             const int h = g * hpg + k;
-            const double A = -(double)expf(__ldg(p.A_log + h));
+            const double A = -exp((double)__ldg(p.A_log + h));
             const float bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.f;
             float d[2];
             double s[2];
@@ -259,8 +324,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
                 mask[64 + i] = (float)(G2 - (double)gh);
                 // times -ln 2: the scan kernel's x is SiLU(x) / -ln 2
                 mask[128 + i] = -kLn2 * d[i];
-                rec[i] = d[i] == 0.f ? 0.f : -kLn2 * (d[i] * expf((float)(all - G)));
-                rec[64 + i] = expf((float)G);
+                rec[i] = d[i] == 0.f ? 0.f : -kLn2 * (d[i] * exp_of(all - G));
+                rec[64 + i] = exp_of(G);
             }
         }
         return;
@@ -290,8 +355,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
         for (int i = 0; i < 3; ++i)
             if (p.init_conv == nullptr && t0 + r0 + i - 3 < start)
                 win[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        __nv_bfloat16 *mine = reinterpret_cast<__nv_bfloat16 *>(smem) + (2 * which * kQ + r0) * LDS + col; // hi; lo is kQ rows on
-        __nv_bfloat16 *out = bc + ((id * p.G + g) * kQ + r0) * (4 * S) + which * 2 * S + col;
+        float most = 0.f;
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
             const float4 ra = win[i], rb = win[i + 1], rc = win[i + 2], rd = win[i + 3];
@@ -305,13 +369,59 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
                 v[k] = silu(v[k]);
             if (r0 + i >= ntok)
                 v[0] = v[1] = v[2] = v[3] = 0.f;
+            most = magnitude_nan(magnitude_nan(most, v[0], v[1]), v[2], v[3]);
+            win[i] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (exponent(most) == 255) { // the largest finite value
+            most = 0.f;
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const float v[4] = {win[i].x, win[i].y, win[i].z, win[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    most = fabsf(v[k]) <= 3.402823466e38f ? fmaxf(most, fabsf(v[k])) : most;
+            }
+        }
+        uint32_t m = (uint32_t)exponent(most);
+        // over the threads of B, and over those of C
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (S == 128)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (lane == 0)
+            largest[which][warp] = m;
+        if (S == 64 ? lane == 16 : lane == 0)
+            largest[S == 64 ? which : 1 - which][warp] = S == 64 ? m : 0u;
+        __syncthreads();
+        m = 0u;
+#pragma unroll
+        for (int i = 0; i < kPrepThreads / 32; ++i)
+            m = max(m, largest[which][i]);
+        const int e = (int)m;
+        const float f = up(which == 0 ? e + 10 : e); // B: 2^3 .. 2^4
+        if (r0 == 0 && col == 0) {
+            const float r = down(which == 0 ? e + 10 : e);
+            back[which] = r;
+            scales[(id * p.G + g) * kScaleRec + which] = r;
+            if (kWhole<T>)
+                cb[(id * p.G + g) * (kQ * kQ) + 16 + which] = r;
+        }
+        uint16_t *mine = reinterpret_cast<uint16_t *>(smem) + (2 * which * kQ + r0) * LDS + col; // hi; lo is kQ rows on
+        uint16_t *out = bc + ((id * p.G + g) * kQ + r0) * (4 * S) + which * 2 * S + col;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
             uint2 h, l;
-            split2(v[0], v[1], h.x, l.x);
-            split2(v[2], v[3], h.y, l.y);
-            *reinterpret_cast<uint2 *>(out + i * (4 * S)) = h;
-            *reinterpret_cast<uint2 *>(out + i * (4 * S) + S) = l;
+            split2<true>(win[i].x * f, win[i].y * f, h.x, l.x);
+            split2<true>(win[i].z * f, win[i].w * f, h.y, l.y);
             *reinterpret_cast<uint2 *>(mine + i * LDS) = h;
             *reinterpret_cast<uint2 *>(mine + (kQ + i) * LDS) = l;
+            if (!kWhole<T> && which == 1) { // C for the read-out
+                split2<false>(win[i].x, win[i].y, h.x, l.x);
+                split2<false>(win[i].z, win[i].w, h.y, l.y);
+            }
+            *reinterpret_cast<uint2 *>(out + i * (4 * S)) = h;
+            *reinterpret_cast<uint2 *>(out + i * (4 * S) + S) = l;
         }
     }
 
@@ -319,6 +429,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
 
     // C B^T: warp w has rows 16 (w % 4) .., columns 16 (w / 4) ..
     const int mt = warp & 3, nt = warp >> 2;
+    uint32_t most = 0u; // the largest product
     if (nt <= mt) {
         float acc[2][4] = {};
         const uint32_t arow = (uint32_t)((mt * 16 + (lane & 15)) * LDS + (lane >> 4) * 8) * 2;
@@ -334,9 +445,22 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
             ldmatrix4(bl, sb + PART + brow + 2 * k);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mma_bf16(acc[i], ah, bh[2 * i], bh[2 * i + 1]);
-                mma_bf16(acc[i], ah, bl[2 * i], bl[2 * i + 1]);
-                mma_bf16(acc[i], al, bh[2 * i], bh[2 * i + 1]);
+                mma_f16(acc[i], ah, bh[2 * i], bh[2 * i + 1]);
+                mma_f16(acc[i], ah, bl[2 * i], bl[2 * i + 1]);
+                mma_f16(acc[i], al, bh[2 * i], bh[2 * i + 1]);
+            }
+        }
+        if (!kWhole<T>) {
+            const float rb = back[0], rc = back[1];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                acc[j / 4][j % 4] = acc[j / 4][j % 4] * rb * rc;
+        }
+        if (kWhole<T>) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t u = __float_as_uint(acc[j / 4][j % 4]) & 0x7fffffffu;
+                most = max(most, u < 0x7f800000u ? u : 0u);
             }
         }
         float *out = cb + (id * p.G + g) * (kQ * kQ) + (mt * 16 + (lane >> 2)) * kQ + nt * 16 + 2 * (lane & 3);
@@ -346,17 +470,29 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ssm_prep_kernel(const SsmArgs
             *reinterpret_cast<float2 *>(out + 8 * kQ + 8 * j) = make_float2(acc[j][2], acc[j][3]);
         }
     }
+    if (kWhole<T>) {
+        most = __reduce_max_sync(0xffffffffu, most);
+        __shared__ uint32_t products[kPrepThreads / 32];
+        if (lane == 0)
+            products[warp] = most;
+        __syncthreads();
+        if (warp == 0) {
+            most = __reduce_max_sync(0xffffffffu, lane < kPrepThreads / 32 ? products[lane] : 0u);
+            if (lane == 0)
+                cb[(id * p.G + g) * (kQ * kQ) + 18] = __uint_as_float(most);
+        }
+    }
 }
 
 // ------------------------------------------------------------------- scan
 
-// Instruction descriptor of a dense kind::f16 MMA, bfloat16 operands, float32 sums.
-constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+// Instruction descriptor of a dense kind::f16 MMA, float16 or bfloat16 operands, float32 sums.
+constexpr uint32_t idesc(bool f16, int M, int N, bool b_mn) {
+    return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
 // D[tmem] (+)= A[tmem] B[smem]^T, one instruction (K = 16), where `issue`.
-__device__ __forceinline__ void mma_bf16_ts_if(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
                                                uint32_t issue) {
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
@@ -407,9 +543,6 @@ template <typename T, int P, int S> struct Scan {
     static constexpr uint32_t kYI2 = 448;          // the other buffer of H C^T
 };
 constexpr int kScanThreads = 640;
-// Chunks of the summary pass that are summed in the accumulators before they are added to the state in registers:
-// sums of 12 MMAs a chunk, which are not rounded to the nearest, should stay few.
-constexpr int kSumChunks = 4;
 constexpr uint32_t kTmemCols = 512;
 
 // B and C slots, M buffers, buffers of C B^T and of raw x, and single barriers
@@ -420,9 +553,9 @@ enum Bar {
 // What a block works on.
 struct Unit {
     int n, seg, tile, h0, nh, g;
-    int64_t start, end;
-    int64_t c0; // first chunk of the segment within the sequence
-    int nc;     // chunks of the segment
+    int start, end; // (there are fewer than 2^31 tokens)
+    int c0;         // first chunk of the segment within the sequence
+    int nc;         // chunks of the segment
 };
 
 template <int P>
@@ -435,16 +568,19 @@ __device__ __forceinline__ Unit unit_of(const SsmArgs &p, int segments, int tile
     const int hpg = p.H / p.G, heads = 128 / P, first = u.tile % tiles_per_group * heads;
     u.h0 = u.g * hpg + first;
     u.nh = min(heads, hpg - first);
-    seq_bounds(p.cu, u.n, p.N, u.start, u.end);
-    const int64_t all = (u.end - u.start + kQ - 1) / kQ;
-    u.c0 = all * u.seg / segments;
-    u.nc = (int)(all * (u.seg + 1) / segments - u.c0);
+    int64_t start, end;
+    seq_bounds(p.cu, u.n, p.N, start, end);
+    u.start = (int)start;
+    u.end = (int)end;
+    const int64_t all = (end - start + kQ - 1) / kQ;
+    u.c0 = (int)(all * u.seg / segments);
+    u.nc = (int)(all * (u.seg + 1) / segments) - u.c0;
     return u;
 }
 
 struct ScanArgs {
     SsmArgs p;
-    const float *cb, *masks, *gates;
+    const float *cb, *masks, *gates, *scales;
     float *seg, *segdecay;
     uint32_t *status;
     int segments, fine, tiles_per_group; // the summary pass cuts every segment into `fine`
@@ -458,7 +594,8 @@ struct ScanArgs {
 // of a scheduler, too few to hide their own latencies.  They meet only through
 // the mbarriers of what they share, so that a warp in its exponentials runs
 // beside one in its splits (with two meetings of all 16 a chunk, and copies of x
-// and z by their own threads, the output pass took 160 us for 145).
+// and z by their own threads, the output pass took 160 us for 145, with bfloat16
+// parts throughout).
 // SUMMARY: only the states of the segments but the last, from zero (the first
 // from the initial state, which is also copied); no output.
 template <typename T, int P, int S, bool SUMMARY>
@@ -470,7 +607,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ __align__(16) float gate[K::kGateSlots][NH][kGateRec], mask[K::kCbBufs][NH][kMaskRec];
-    __shared__ __align__(4) uint8_t bad[2][128][4]; // per row and 16 tokens: the first with a non-finite x, or kQ
+    __shared__ __align__(16) float bcscale[K::kGateSlots][kScaleRec]; // what B and C of a chunk are to be multiplied with
+    __shared__ float mscale[4][NH]; // and M of each head (M runs up to two chunks ahead of its reader)
+    // What a row's four working threads tell each other: the exponent fields of their largest |x'| and, in the low byte
+    // and halved, |x|, with 0x80 if some x is not finite.  (The summary pass: those of |x'|, in two buffers in turn.)
+    __shared__ __align__(8) uint16_t told[128][4];
     __shared__ uint32_t tmem_base, abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint8_t *sm = smem_raw + (base - smem_u32(smem_raw));
@@ -546,7 +687,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             mbar_arrive(bar(i));
     };
     auto i_done = [&](int c, bool patient = false) { return wait_all(kIDone + (c & 1), (c >> 1) & 1, patient); };
-    const int64_t tok0 = u.start + u.c0 * kQ;
+    const int tok0 = u.start + u.c0 * kQ;
     // raw x: the summary pass has two buffers
     auto raw_slot = [](int c) { return SUMMARY ? c & 1 : 0; };
     auto raw_phase = [](int c) { return (uint32_t)(SUMMARY ? c >> 1 : c) & 1; };
@@ -592,7 +733,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         if (!(ok = wait(kZEmpty, (c & 1) ^ 1) && !*abort_v))
                             break;
                         mbar_arrive_expect_tx(bar(kZFull), kQ * K::kRow);
-                        tma_load_2d(base + K::kOffZ, &tz, u.h0 * P, (int)(tok0 + (int64_t)(c - 2) * kQ), bar(kZFull));
+                        tma_load_2d(base + K::kOffZ, &tz, u.h0 * P, tok0 + (c - 2) * kQ, bar(kZFull));
                         ++zs;
                     }
                     if (c < u.nc) {
@@ -600,9 +741,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         if (!(ok = wait(kRawEmpty + rs, raw_phase(c) ^ 1) && !*abort_v))
                             break;
                         // (x's room is free, so the weights of the chunk four before are done with too)
-                        mbar_arrive_expect_tx(bar(kRawFull + rs), K::kXBytes + gbytes);
+                        mbar_arrive_expect_tx(bar(kRawFull + rs), K::kXBytes + gbytes + kScaleRec * 4);
+                        bulk_load(smem_u32(bcscale[c % K::kGateSlots]), a.scales + ((id0 + at) * p.G + u.g) * kScaleRec, kScaleRec * 4, bar(kRawFull + rs));
                         bulk_load(smem_u32(gate[c % K::kGateSlots]), a.gates + ((id0 + at) * p.H + u.h0) * kGateRec, gbytes, bar(kRawFull + rs));
-                        tma_load_2d(base + (rs ? K::kOffX2 : K::kOffX), &tx, u.h0 * P, (int)(tok0 + (int64_t)at * kQ) - 3, bar(kRawFull + rs));
+                        tma_load_2d(base + (rs ? K::kOffX2 : K::kOffX), &tx, u.h0 * P, tok0 + at * kQ - 3, bar(kRawFull + rs));
                         ++raws;
                         if (!SUMMARY) {
                             const int cs = c % K::kCbBufs;
@@ -648,19 +790,19 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 }
             };
             for (int c = 0; SUMMARY && c < u.nc; ++c) {
-                // D[row][s] (+)= sum_t x'[row][t] B[t][s], two buffers of x' and of D
+                // D[row][s] = sum_t x'[row][t] B[t][s], two buffers of x' and of D
                 ok = wait_all(kBcFull + slot, sph) && wait_all(c & 1 ? kXFull : kHFull, (c >> 1) & 1);
                 if (!ok)
                     break;
                 tc_fence_after();
-                const uint32_t bh = base + slot * K::kHalf, bl = bh + S * 128, d = tmem + K::kDH + ((c / kSumChunks) & 1) * 128;
+                const uint32_t bh = base + slot * K::kHalf, bl = bh + S * 128, d = tmem + K::kDH + (c & 1) * 128;
 #pragma unroll
                 for (int kk = 0; kk < kQ / 16; ++kk) {
                     const uint32_t xh = tmem + (c & 1 ? K::kX : K::kXP) + 8 * kk, xl = xh + 32;
-                    mma_bf16_ts_if(d, xh, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true),
-                                   kk > 0 || c % kSumChunks > 0, issue);
-                    mma_bf16_ts_if(d, xh, sdesc_sw128(bl + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
-                    mma_bf16_ts_if(d, xl, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
+                    mma_f16_ts_if(d, xh, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc(true, 128, S, true),
+                                   kk > 0, issue);
+                    mma_f16_ts_if(d, xh, sdesc_sw128(bl + 2048 * kk, 8192, 1024), idesc(true, 128, S, true), 1, issue);
+                    mma_f16_ts_if(d, xl, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc(true, 128, S, true), 1, issue);
                 }
                 mma_commit_if(bar(kIDone + (c & 1)), issue);
                 mma_commit_if(bar(kBcEmpty + slot), issue);
@@ -681,9 +823,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 for (int kk = 0; kk < S / 16; ++kk) {
                     const uint32_t hh = tmem + K::kDH + kk / (CW / 16) * CW + kk % (CW / 16) * 8, hlo = hh + CW / 2;
                     const uint32_t off = kk / 4 * 8192 + kk % 4 * 32;
-                    mma_bf16_ts_if(yi, hh, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), kk > 0, issue);
-                    mma_bf16_ts_if(yi, hh, sdesc_sw128(cl + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
-                    mma_bf16_ts_if(yi, hlo, sdesc_sw128(ch + off, 16, 1024), idesc_bf16(128, 64, false), 1, issue);
+                    mma_f16_ts_if(yi, hh, sdesc_sw128(ch + off, 16, 1024), idesc(kWhole<T>, 128, 64, false), kk > 0, issue);
+                    mma_f16_ts_if(yi, hh, sdesc_sw128(cl + off, 16, 1024), idesc(kWhole<T>, 128, 64, false), 1, issue);
+                    mma_f16_ts_if(yi, hlo, sdesc_sw128(ch + off, 16, 1024), idesc(kWhole<T>, 128, 64, false), 1, issue);
                 }
                 mma_commit_if(bar(kBcEmpty + slot), issue);
                 next_slot();
@@ -696,9 +838,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll 1
                 for (int kk = 0; kk < kQ / 16; ++kk) {
                     const uint32_t xh = tmem + K::kXP + 8 * kk, xl = xh + 32;
-                    mma_bf16_ts_if(tmem + K::kDH, xh, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), kk > 0, issue);
-                    mma_bf16_ts_if(tmem + K::kDH, xh, sdesc_sw128(bl + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
-                    mma_bf16_ts_if(tmem + K::kDH, xl, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc_bf16(128, S, true), 1, issue);
+                    mma_f16_ts_if(tmem + K::kDH, xh, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc(true, 128, S, true), kk > 0, issue);
+                    mma_f16_ts_if(tmem + K::kDH, xh, sdesc_sw128(bl + 2048 * kk, 8192, 1024), idesc(true, 128, S, true), 1, issue);
+                    mma_f16_ts_if(tmem + K::kDH, xl, sdesc_sw128(bh + 2048 * kk, 8192, 1024), idesc(true, 128, S, true), 1, issue);
                 }
                 mma_commit_if(bar(kUDone), issue);
                 mma_commit_if(bar(kBcEmpty + slot), issue);
@@ -715,9 +857,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll 1
                 for (int kk = 0; kk < kQ / 16; ++kk) {
                     const uint32_t xh = tmem + K::kX + 8 * kk, xl = xh + 32;
-                    mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), kk > 0, issue);
-                    mma_bf16_ts_if(tmem + K::kYA, xh, sdesc_sw128(ml + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
-                    mma_bf16_ts_if(tmem + K::kYA, xl, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc_bf16(128, 64 * NH, false), 1, issue);
+                    mma_f16_ts_if(tmem + K::kYA, xh, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc(kWhole<T>, 128, 64 * NH, false), kk > 0, issue);
+                    mma_f16_ts_if(tmem + K::kYA, xh, sdesc_sw128(ml + 32 * kk, 16, 1024), idesc(kWhole<T>, 128, 64 * NH, false), 1, issue);
+                    mma_f16_ts_if(tmem + K::kYA, xl, sdesc_sw128(mh + 32 * kk, 16, 1024), idesc(kWhole<T>, 128, 64 * NH, false), 1, issue);
                 }
                 mma_commit_if(bar(kIDone + (c & 1)), issue);
             }
@@ -726,14 +868,43 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             mbar_wait_sleeping(bar(kDrain), 0, kDefaultWaitLimit);
         } else { // ---- M: the decay masks times C B^T, as operands; two warps
             const int odd = lane & 1; // a thread has a row and every other group of 8 columns
-            const float D0 = p.D != nullptr ? -kLn2 * __ldg(p.D + u.h0) : 0.f;
-            const float D1 = p.D != nullptr && u.nh > 1 ? -kLn2 * __ldg(p.D + u.h0 + 1) : 0.f;
+            float D[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+                D[h] = p.D != nullptr && h < u.nh ? -kLn2 * __ldg(p.D + u.h0 + h) : 0.f;
             for (int c = 0; c < (SUMMARY ? 0 : u.nc); ++c) {
                 const int mb = c % K::kMBufs, cs = c % K::kCbBufs;
                 // the chunk that last had this buffer: its products are done
                 if (!wait_all(kCbFull + cs, (c / K::kCbBufs) & 1, true) || (c >= K::kMBufs && !i_done(c - K::kMBufs, true)))
                     break;
                 const uint32_t mbuf = base + K::kOffM + mb * K::kMBytes;
+                float fm[NH], Ds[NH];
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    fm[h] = 1.f;
+                    Ds[h] = D[h];
+                }
+                if (kWhole<T>) {
+                    // the largest C . B times the largest delta, of which no mask is above 1, brought to 2^15 at most; D, which
+                    // is to be added to it, may ask for less
+                    const uint8_t *factors = sm + K::kOffCb + cs * K::kCbBytes + 64; // (row 0, column 16)
+                    const int bc = 254 - exponent(*reinterpret_cast<const float *>(factors)) - exponent(*reinterpret_cast<const float *>(factors + 4));
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        uint32_t most = 0u;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t v = __float_as_uint(mask[cs][h][128 + 2 * lane + k]) & 0x7fffffffu;
+                            most = max(most, v < 0x7f800000u ? v : 0u);
+                        }
+                        const int m = 267 - exponent(*reinterpret_cast<const float *>(factors + 8)) - (int)(__reduce_max_sync(0xffffffffu, most) >> 23);
+                        const int n = max(min(min(bc + m, 141 - exponent(D[h])), 126), -126);
+                        fm[h] = pow2(n - bc);
+                        Ds[h] = D[h] * pow2(n);
+                        if (warp == 2 && lane == 0)
+                            mscale[c & 3][h] = pow2(-n);
+                    }
+                }
                 // 16-blocks (row, column): (0, 0) (3, 0) (3, 1) (3, 2) (3, 3) of one warp, (1, 0) (1, 1) (2, 0)
                 // (2, 1) (2, 2) of the other
 #pragma unroll 1 // (unrolled: 223 us for 197 at 4096 tokens, for the same reason)
@@ -750,7 +921,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
                     for (int h = 0; h < NH; ++h) { // an absent head's mask is never used
                         const float *rec = mask[cs][h];
-                        const float gh = rec[t], gl = rec[64 + t], Dh = h == 0 ? D0 : D1;
+                        const float gh = rec[t], gl = rec[64 + t], Dh = Ds[h], f = fm[h];
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int k = 0; k < 8; k += 4) {
@@ -758,18 +929,18 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             const float4 sl = *reinterpret_cast<const float4 *>(rec + 64 + s0 + k);
                             const float4 sd = *reinterpret_cast<const float4 *>(rec + 128 + s0 + k);
                             float m[4];
-                            m[0] = ex2((gh - sh.x) + (gl - sl.x)) * (sd.x * v[k]);
-                            m[1] = ex2((gh - sh.y) + (gl - sl.y)) * (sd.y * v[k + 1]);
-                            m[2] = ex2((gh - sh.z) + (gl - sl.z)) * (sd.z * v[k + 2]);
-                            m[3] = ex2((gh - sh.w) + (gl - sl.w)) * (sd.w * v[k + 3]);
+                            m[0] = ex2((gh - sh.x) + (gl - sl.x)) * ((kWhole<T> ? sd.x * f : sd.x) * v[k]);
+                            m[1] = ex2((gh - sh.y) + (gl - sl.y)) * ((kWhole<T> ? sd.y * f : sd.y) * v[k + 1]);
+                            m[2] = ex2((gh - sh.z) + (gl - sl.z)) * ((kWhole<T> ? sd.z * f : sd.z) * v[k + 2]);
+                            m[3] = ex2((gh - sh.w) + (gl - sl.w)) * ((kWhole<T> ? sd.w * f : sd.w) * v[k + 3]);
                             if (i == rb) { // the diagonal block
                                 const int at = t - s0 - k; // the diagonal's column among the four
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
                                     m[j] = at < j ? 0.f : at == j ? m[j] + Dh : m[j];
                             }
-                            split2(m[0], m[1], hi[k / 2], lo[k / 2]);
-                            split2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
+                            split2<kWhole<T>>(m[0], m[1], hi[k / 2], lo[k / 2]);
+                            split2<kWhole<T>>(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
                         }
                         // K-major rows of 128 bytes, 16-byte pieces swizzled by the row
                         const uint32_t at = mbuf + h * kQ * kQ * 2 + t * 128 + (((s0 >> 3) ^ (t & 7)) << 4);
@@ -820,7 +991,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         // the barriers, with the flag set before: the loading thread looks at that before it loads over x or z.)
         bool ok = true;
         // x of the chunk of tokens t0 .., the i-th that is loaded: tokens 16 part ..
-        auto take_x = [&](int i, int64_t t0, float (&x)[16]) {
+        auto take_x = [&](int i, int t0, float (&x)[16]) {
             const int rs = raw_slot(i);
             ok = ok && wait_all(kRawFull + rs, raw_phase(i));
             float r[19]; // tokens -3, .., 15
@@ -839,7 +1010,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
             for (int t = 0; t < 16; ++t)
                 x[t] = silu_scaled(fmaf(w3, r[t + 3], fmaf(w2, r[t + 2], fmaf(w1, r[t + 1], fmaf(w0, r[t], wb)))));
-            const int valid = live ? (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part : 0;
+            const int valid = live ? min(u.end - t0, kQ) - 16 * part : 0;
             if (valid < 16) {
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
@@ -847,19 +1018,59 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         x[t] = 0.f;
             }
         };
-        // h = f h + the accumulator at column `at`
-        auto add_acc = [&](float f, uint32_t at) {
-            const f2 ff = pack(f, f);
+        // h = f h + r times the accumulator at column `at`; r (or f) of 1 costs nothing
+        auto add_acc = [&](auto f, auto r, uint32_t at) {
+            constexpr bool F = std::is_same<decltype(f), float>::value, R = std::is_same<decltype(r), float>::value;
+            const f2 ff = pack((float)f, (float)f), rr = pack((float)r, (float)r);
 #pragma unroll
             for (int i = 0; i < CW; i += 16) {
                 float v[16];
                 tmem_ld16(tmem + lanes + at + CW * part + i, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    h[i / 2 + k] = fma2(ff, h[i / 2 + k], pack(v[2 * k], v[2 * k + 1]));
+                for (int k = 0; k < 8; ++k) {
+                    const f2 u = pack(v[2 * k], v[2 * k + 1]);
+                    if (F && R)
+                        h[i / 2 + k] = fma2(ff, h[i / 2 + k], mul2(rr, u));
+                    else
+                        h[i / 2 + k] = F ? fma2(ff, h[i / 2 + k], u) : fma2(rr, u, h[i / 2 + k]);
+                }
             }
         };
+        // The four warps of the same rows meet: what each told is there for the others.
+        auto meet = [&]() { __syncwarp(); asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); };
+        auto told_by_all = [&]() { return *reinterpret_cast<const uint2 *>(told[row]); };
+        // x' = x w
+        auto weigh = [&](const float (&x)[16], const float4 *wt, f2 (&xw)[8]) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                const ulonglong2 w = reinterpret_cast<const ulonglong2 *>(wt)[k / 2];
+                xw[k] = mul2(pack(x[2 * k], x[2 * k + 1]), w.x);
+                xw[k + 1] = mul2(pack(x[2 * k + 2], x[2 * k + 3]), w.y);
+            }
+        };
+        auto largest = [&](const f2 (&v)[8]) {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 f = unpack(v[k]);
+                m = magnitude(m, f.x, f.y);
+            }
+            return m;
+        };
+        // f v in float16 parts, or v in bfloat16 parts, as an operand at column `to`
+        auto put = [&](auto f16, const f2 (&v)[8], float f, uint32_t to) {
+            const f2 ff = pack(f, f);
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 u = unpack(f16.value ? mul2(ff, v[k]) : v[k]);
+                split2<f16.value>(u.x, u.y, hi[k], lo[k]);
+            }
+            tmem_st8(tmem + lanes + to + 8 * part, hi);
+            tmem_st8(tmem + lanes + to + 32 + 8 * part, lo);
+        };
+        using whole = std::integral_constant<bool, kWhole<T>>;
 #pragma unroll
         for (int i = 0; i < CW / 2; ++i)
             h[i] = 0ull;
@@ -872,32 +1083,29 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 for (int i = 0; i < CW / 2; ++i)
                     h[i] = 0ull;
             }
-            // Backwards, so that the decay from a chunk to the segment's end is known when its x' is made: the
-            // chunks' shares are then summed as they are, kSumChunks of them in the accumulators.
-            float decay = 1.f;
+            // Backwards: a chunk's share is taken times the decay from its end to the segment's.
+            float decay = 1.f, r0 = 0.f, r1 = 0.f; // r0, r1: what U of the last chunk and of the one before is to be multiplied with
 #pragma unroll 1
             for (int c = 0; c < u.nc; ++c) {
                 float x[16];
-                take_x(c, tok0 + (int64_t)(u.nc - 1 - c) * kQ, x);
+                take_x(c, tok0 + (u.nc - 1 - c) * kQ, x);
+                const float *rec = gate[c % K::kGateSlots][hl];
+                const float4 *wt = reinterpret_cast<const float4 *>(rec + 16 * part);
+                f2 xw[8];
+                weigh(x, wt, xw);
+                reinterpret_cast<uint8_t *>(told[row])[4 * (c & 1) + part] = (uint8_t)exponent(largest(xw));
                 if (c >= 2) {
                     ok = ok && i_done(c - 2);
                     tc_fence_after();
-                    if (c % kSumChunks == 1)
-                        add_acc(1.f, K::kDH + ((c / kSumChunks - 1) & 1) * 128);
+                    add_acc(1, r1, K::kDH + (c & 1) * 128);
                 }
-                const float *rec = gate[c % K::kGateSlots][hl];
-                const float4 *wt = reinterpret_cast<const float4 *>(rec + 16 * part);
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    const float4 w = wt[k / 2];
-                    split2(x[2 * k] * (w.x * decay), x[2 * k + 1] * (w.y * decay), hi[k], lo[k]);
-                    split2(x[2 * k + 2] * (w.z * decay), x[2 * k + 3] * (w.w * decay), hi[k + 1], lo[k + 1]);
-                }
+                meet();
+                const uint32_t t = reinterpret_cast<const uint32_t *>(told[row])[c & 1];
+                const int e = largest_half(t & 0x00ff00ffu, (t >> 8) & 0x00ff00ffu);
+                put(std::true_type(), xw, up(e), c & 1 ? K::kX : K::kXP);
+                r1 = r0;
+                r0 = down(e) * bcscale[c % K::kGateSlots][0] * decay;
                 decay *= live ? rec[64 + 63] : 0.f;
-                const uint32_t to = tmem + lanes + (c & 1 ? K::kX : K::kXP) + 8 * part;
-                tmem_st8(to, hi);
-                tmem_st8(to + 32, lo);
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(c & 1 ? kXFull : kHFull);
@@ -905,10 +1113,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             if (u.nc > 0) {
                 ok = ok && i_done(u.nc - 1);
                 tc_fence_after();
-                const int last = (u.nc - 1) / kSumChunks;
-                if ((u.nc - 1) % kSumChunks == 0 && last > 0)
-                    add_acc(1.f, K::kDH + ((last - 1) & 1) * 128);
-                add_acc(1.f, K::kDH + (last & 1) * 128);
+                if (u.nc > 1)
+                    add_acc(1, r1, K::kDH + (u.nc & 1) * 128);
+                add_acc(1, r0, K::kDH + ((u.nc - 1) & 1) * 128);
             }
             if (u.seg == 0 && live && p.init_state != nullptr)
                 add_state(p.init_state + gstate, 4, 1.f, decay);
@@ -929,21 +1136,83 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 for (int s = 2; s <= to; ++s)
                     add_state(seg_at(s), kApart, a.segdecay[(unit0 + s - 1) * 2 + hl], 1.f);
             }
+            // A bound of the row's |H|: the largest of the state that enters, then with every chunk gamma times it and 64
+            // times the largest x' and B.  It may be far above H, but above the sum of the magnitudes that make H up only by
+            // as much as x' and B vary.  The state is kept scaled by it, and x' so that U comes out in the state's units.
+            float bound = 0.f;
+            auto scale_state = [&](float f) {
+                const f2 ff = pack(f, f);
+#pragma unroll
+                for (int i = 0; i < CW / 2; ++i)
+                    h[i] = mul2(ff, h[i]);
+            };
+            if (kWhole<T>) {
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < CW / 2; ++i) {
+                    const float2 v = unpack(h[i]);
+                    m = fabsf(v.x) <= 3.402823466e38f ? fmaxf(m, fabsf(v.x)) : m;
+                    m = fabsf(v.y) <= 3.402823466e38f ? fmaxf(m, fabsf(v.y)) : m;
+                }
+                told[row][part] = (uint16_t)exponent(m);
+                meet();
+                const uint2 t = told_by_all();
+                bound = pow2(largest_half(t.x, t.y) - 126);
+                meet();
+                scale_state(up(exponent(bound)));
+            }
+            // kWhole: gamma in the state's units, from those before chunk c to those after it; else what its U is to be
+            // multiplied with
+            float step = 0.f;
+            // exponent fields of the row's largest x of a chunk and of the bound before it, and the first token here whose x
+            // or an earlier one is not finite, by bytes
+            uint32_t now = 0u;
 #pragma unroll 1
             for (int c = -1; c < u.nc; ++c) {
                 const bool more = c + 1 < u.nc;
-                const int64_t t0 = tok0 + (int64_t)c * kQ; // of chunk c
+                const int t0 = tok0 + c * kQ; // of chunk c
+                const int slot = c & (K::kGateSlots - 1), next = (c + 1) & (K::kGateSlots - 1);
                 // -- x of chunk c + 1: tokens 16 part ..
                 float x[16];
-                if (more)
+                const float4 *wt = reinterpret_cast<const float4 *>(gate[next][hl] + 16 * part);
+                f2 xw[8];
+                uint32_t mine = 0u; // what this thread tells, and its first x that is not finite
+                if (more) {
                     take_x(c + 1, t0 + kQ, x);
+                    weigh(x, wt, xw);
+                    mine = (uint32_t)exponent(largest(xw)) << 8;
+                    float mx = 0.f;
+                    uint32_t first = 16;
+#pragma unroll
+                    for (int t = 0; t < 16; t += 2)
+                        mx = magnitude_nan(mx, x[t], x[t + 1]);
+                    if (exponent(mx) == 255) {
+                        mx = 0.f;
+#pragma unroll
+                        for (int t = 15; t >= 0; --t) {
+                            if (!(fabsf(x[t]) <= 3.402823466e38f))
+                                first = t;
+                            else
+                                mx = fmaxf(mx, fabsf(x[t]));
+                        }
+                        mine |= 0x80;
+                    }
+                    mine |= (kWhole<T> ? (uint32_t)exponent(mx) >> 1 : 0u) | first << 24;
+                }
                 // -- the state entering chunk c + 1, and x' of that chunk
                 if (c >= 0) {
                     ok = ok && wait_all(kUDone, c & 1);
                     tc_fence_after();
-                    const float gamma = live ? gate[c % K::kGateSlots][hl][64 + 63] : 0.f;
-                    add_acc(gamma, K::kDH);
                 }
+                if (more) // (all four have read what was told before, or U would not be done)
+                    told[row][part] = (uint16_t)mine;
+                if (c >= 0) {
+                    if constexpr (kWhole<T>)
+                        add_acc(step, 1, K::kDH);
+                    else
+                        add_acc(live ? gate[slot][hl][64 + 63] : 0.f, step, K::kDH);
+                }
+                uint32_t then = 0u;
                 if (more) {
 #pragma unroll
                     for (int i = 0; i < CW; i += 16) {
@@ -951,68 +1220,81 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const float2 v = unpack(h[i / 2 + k]);
-                            split2(v.x, v.y, hi[k], lo[k]);
+                            split2<kWhole<T>>(v.x, v.y, hi[k], lo[k]);
                         }
                         tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
                         tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
                     }
-                    const float4 *wt = reinterpret_cast<const float4 *>(gate[(c + 1) % K::kGateSlots][hl] + 16 * part);
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int k = 0; k < 8; k += 2) {
-                        const float4 w = wt[k / 2];
-                        split2(x[2 * k] * w.x, x[2 * k + 1] * w.y, hi[k], lo[k]);
-                        split2(x[2 * k + 2] * w.z, x[2 * k + 3] * w.w, hi[k + 1], lo[k + 1]);
+                    meet();
+                    const uint2 t = told_by_all();
+                    const int ew = largest_half(t.x, t.y) >> 8;
+                    then = mine & 0xff000000u;
+                    if (kWhole<T>)
+                        then |= (uint32_t)(2 * largest_half(t.x & 0x007f007fu, t.y & 0x007f007fu) + 1) | (uint32_t)exponent(bound) << 8;
+                    if ((t.x | t.y) & 0x00800080u) { // some x is not finite: in an earlier part?
+                        const uint32_t bad = (t.x & 0x80u) >> 7 | (t.x & 0x800000u) >> 22 | (t.y & 0x80u) >> 5 | (t.y & 0x800000u) >> 20;
+                        if (bad & ((1u << part) - 1u))
+                            then &= 0xffffffu;
                     }
-                    tmem_st8(tmem + lanes + K::kXP + 8 * part, hi);
-                    tmem_st8(tmem + lanes + K::kXP + 32 + 8 * part, lo);
+                    const float fb = bcscale[next][0];
+                    float f = up(ew);
+                    if (kWhole<T>) {
+                        // x' is below 2^(ew - 126) and B below 2^4 times its factor (x' of zeros must not ask for infinity)
+                        const float gamma = live ? gate[next][hl][64 + 63] : 0.f, back = down(exponent(bound));
+                        bound = fmaf(gamma, bound, pow2(max(ew, 24) - 116) * fb);
+                        f = up(exponent(bound));
+                        step = gamma * f * back;
+                        f *= fb;
+                    } else {
+                        step = down(ew) * fb;
+                    }
+                    if (S == 128) // again: 128 columns leave no registers to keep it
+                        weigh(x, wt, xw);
+                    put(std::true_type(), xw, f, K::kXP);
                     tmem_wait_st();
                     tc_fence_before();
                     arrive(kHFull);
                 }
                 // -- the output of chunk c out of the accumulators, and x of chunk c + 1 as operand
                 float y[16];
-                uint32_t nf = 0; // the first bad tokens of chunk c, by parts
                 if (c >= 0) {
-                    ok = ok && i_done(c); // the MMAs waited for kXFull, so the other parts' first bad tokens are here too
-                    nf = *reinterpret_cast<const uint32_t *>(bad[c & 1][row]);
+                    ok = ok && i_done(c);
                     tc_fence_after();
                     float e[16];
                     tmem_ld16(tmem + lanes + ((c & 1) ? K::kYI2 : K::kYI) + 16 * part, y);
                     tmem_ld16(tmem + lanes + K::kYA + 64 * hl + 16 * part, e);
                     tmem_wait_ld();
-                    const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[c % K::kGateSlots][hl] + 64 + 16 * part);
+                    const float ry = down((now >> 8) & 0xff) * bcscale[slot][1], rm = down(now & 0xff) * mscale[c & 3][hl];
+                    const f2 ry2 = pack(ry, ry), rm2 = pack(rm, rm);
+                    const ulonglong2 *eg = reinterpret_cast<const ulonglong2 *>(gate[slot][hl] + 64 + 16 * part);
+                    // e^G times the state's part, and the masks' part
+                    auto sum = [&](f2 f, f2 state, f2 masks) {
+                        return unpack(kWhole<T> ? fma2(mul2(f, ry2), state, mul2(rm2, masks)) : fma2(f, state, masks));
+                    };
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
                         const ulonglong2 f = eg[k / 4];
-                        const float2 a0 = unpack(fma2(f.x, pack(y[k], y[k + 1]), pack(e[k], e[k + 1])));
-                        const float2 a1 = unpack(fma2(f.y, pack(y[k + 2], y[k + 3]), pack(e[k + 2], e[k + 3])));
+                        const float2 a0 = sum(f.x, pack(y[k], y[k + 1]), pack(e[k], e[k + 1]));
+                        const float2 a1 = sum(f.y, pack(y[k + 2], y[k + 3]), pack(e[k + 2], e[k + 3]));
                         y[k] = a0.x; y[k + 1] = a0.y; y[k + 2] = a1.x; y[k + 3] = a1.y;
                     }
                 }
+                const uint32_t bad = now >> 24;
+                now = then;
                 if (more) {
                     // A non-finite x would reach the tokens before it in its chunk (as 0 times it): the
                     // product takes 0 instead, and the output is set from that token on.
-                    float zero = 0.f;
+                    if ((now >> 24) < 16) {
 #pragma unroll
-                    for (int t = 0; t < 16; ++t)
-                        zero = fmaf(x[t], 0.f, zero);
-                    int first = kQ;
-                    if (zero != 0.f) {
-#pragma unroll
-                        for (int t = 15; t >= 0; --t)
-                            if (!(fabsf(x[t]) <= 3.402823466e38f)) {
-                                first = 16 * part + t;
+                        for (int t = 0; t < 16; ++t)
+                            if (!(fabsf(x[t]) <= 3.402823466e38f))
                                 x[t] = 0.f;
-                            }
                     }
-                    bad[(c + 1) & 1][row][part] = (uint8_t)first;
-                    uint32_t hi[8], lo[8];
+                    f2 xs[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
-                    tmem_st8(tmem + lanes + K::kX + 8 * part, hi);
-                    tmem_st8(tmem + lanes + K::kX + 32 + 8 * part, lo);
+                        xs[k] = pack(x[2 * k], x[2 * k + 1]);
+                    put(whole(), xs, up((int)(now & 0xff)), K::kX);
                     tmem_wait_st();
                     tc_fence_before();
                     arrive(kXFull);
@@ -1020,13 +1302,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 if (c < 0)
                     continue;
                 // -- the output of chunk c: gate and store
-                if (nf != 0x40404040u) {
-                    int first = kQ; // the first bad token up to this part's end
-                    for (int k = 0; k <= part; ++k)
-                        first = min(first, (int)(nf >> (8 * k)) & 0xff);
+                if (bad < 16) {
 #pragma unroll
                     for (int t = 0; t < 16; ++t)
-                        if (16 * part + t >= first)
+                        if (t >= (int)bad)
                             y[t] = __uint_as_float(0x7fffffffu);
                 }
                 // through shared memory, over z where there is one, so that a warp stores its 32 channels of 8 tokens
@@ -1047,10 +1326,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 __syncwarp();
                 if (live) {
                     constexpr int LANES = 2 * (int)sizeof(T), ROWS = 32 / LANES; // lanes of a row's 32 channels, rows at once
-                    const int valid = (int)(u.end - t0 < kQ ? u.end - t0 : kQ) - 16 * part;
+                    const int valid = min(u.end - t0, kQ) - 16 * part;
                     const int t = lane / LANES, k = lane % LANES;
                     const uint8_t *from = sm + K::kOffZ + (16 * part + t) * K::kRow + 32 * q * (int)sizeof(T) + 16 * k;
-                    char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + (t0 + 16 * part + t) * ys + u.h0 * P + 32 * q) + 16 * k;
+                    char *dst = reinterpret_cast<char *>(reinterpret_cast<T *>(p.y) + (int64_t)(t0 + 16 * part + t) * ys + u.h0 * P + 32 * q) + 16 * k;
 #pragma unroll
                     for (int i = 0; i < 16; i += ROWS) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(from + i * K::kRow);
@@ -1065,8 +1344,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     __syncwarp();
                 }
             }
-            if (ok && u.seg == a.segments - 1 && live && p.final_state != nullptr)
+            if (ok && u.seg == a.segments - 1 && live && p.final_state != nullptr) {
+                if (kWhole<T>)
+                    scale_state(down(exponent(bound)));
                 store_state(p.final_state + gstate, 4);
+            }
         }
     }
     __syncwarp();
@@ -1099,12 +1381,12 @@ template <typename T> __global__ void __launch_bounds__(256) ssm_final_conv_kern
 // summary pass before it cuts each into.  The lengths are on the device, so that
 // the choice knows their sum only; of several sequences the longest is taken to
 // have 2.3 times the mean (that of five cut at random).  Costs are in chunks of
-// the output pass, 4.3 us: a chunk of the summary pass takes 1.2 us, a block
+// the output pass, 4.5 us: a chunk of the summary pass takes 1.3 us, a block
 // about 6 us to start and end, the summary pass 13 us by itself.
 // Measured with 32 heads of 64 and 128 states, 1 and the chosen number of
-// segments: 1024 tokens 84 and 49 us (8); 4096, 64, 64, 64 tokens 262 and 119
-// (4); 512, 512 57 and 48 (4); what it costs where the lengths are alike after
-// all: four of 700 tokens 69 and 78 (4).
+// segments: 1024 tokens 80 and 36 us (8); 4096, 64, 64, 64 tokens 284 and 117
+// (4); 512, 512 48 and 34 (4); what it costs where the lengths are alike after
+// all: four of 700 tokens 64 and 68 (4).
 struct Cut {
     int segments, fine;
 };
@@ -1144,13 +1426,13 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
     const int tpg = (p.H / p.G * P + 127) / 128;
     const int64_t chunks = max_chunks(p.N, p.batch);
     cudaError_t e = cudaSuccess;
-    ScanArgs a{p, (float *)(ws + l.cb), (float *)(ws + l.masks), (float *)(ws + l.gates), (float *)(ws + l.seg), (float *)(ws + l.segdecay), status, p.segments, p.fine, tpg};
+    ScanArgs a{p, (float *)(ws + l.cb), (float *)(ws + l.masks), (float *)(ws + l.gates), (float *)(ws + l.scales), (float *)(ws + l.seg), (float *)(ws + l.segdecay), status, p.segments, p.fine, tpg};
     if (p.N > 0) {
         e = cudaFuncSetAttribute(ssm_prep_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem<S>());
         if (e != cudaSuccess)
             return e;
         ssm_prep_kernel<T, S><<<dim3((unsigned)chunks, p.G, 2), kPrepThreads, prep_smem<S>(), s>>>(
-            p, (__nv_bfloat16 *)(ws + l.bc), (float *)(ws + l.cb), (float *)(ws + l.masks), (float *)(ws + l.gates), status);
+            p, (uint16_t *)(ws + l.bc), (float *)(ws + l.cb), (float *)(ws + l.masks), (float *)(ws + l.gates), (float *)(ws + l.scales), status);
         e = cudaGetLastError();
         if (e == cudaSuccess)
             e = record_if(begin, s);
@@ -1159,7 +1441,7 @@ template <typename T, int P, int S> cudaError_t launch_t(const SsmArgs &p, cudaE
         CUtensorMap tbc, tcb, tx, tz{};
         const CUtensorMapDataType type = sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
         if (!encode_2d(&tbc, ws + l.bc, 4 * S, (uint64_t)chunks * p.G * kQ, 4 * S * 2, 64, kQ, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
+                       CU_TENSOR_MAP_DATA_TYPE_FLOAT16) ||
             !encode_2d(&tcb, ws + l.cb, kQ, (uint64_t)chunks * p.G * kQ, kQ * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !encode_2d(&tx, p.xbc, p.conv_dim(), p.N, p.xbc_stride * sizeof(T), 128, kQ + 3, CU_TENSOR_MAP_SWIZZLE_NONE, type) ||
             (p.z != nullptr && !encode_2d(&tz, p.z, (uint64_t)p.H * P, p.N, p.z_stride * sizeof(T), 128, kQ, CU_TENSOR_MAP_SWIZZLE_NONE, type)))
