@@ -18,8 +18,8 @@
 // With few sequences each is cut into segments, and a first run of the scan
 // kernel, without outputs, finds what each segment adds to the state.
 //
-// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 212 us (by
-// themselves: prep 31, summary 42, output pass 148), where moving the bytes would
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 210 us (by
+// themselves: prep 31, summary 42, output pass 145), where moving the bytes would
 // take 35 and the MMAs 50.  What bounds it is the 16 warps' instructions and their
 // latency: two thirds of the issue slots, four such warps to a scheduler (the
 // splits, the convolution, two SiLUs); the tensor core is busy for a quarter.
@@ -547,7 +547,7 @@ constexpr uint32_t kTmemCols = 512;
 
 // B and C slots, M buffers, buffers of C B^T and of raw x, and single barriers
 enum Bar {
-    kBcFull = 0, kBcEmpty = 3, kMFull = 6, kIDone = 8, kCbFull = 10, kCbEmpty = 12, kRawFull = 14, kRawEmpty = 16, kHFull = 18, kXFull, kUDone, kDrain, kZFull, kZEmpty, kBars
+    kBcFull = 0, kBcEmpty = 3, kMFull = 6, kIDone = 8, kCbFull = 10, kCbEmpty = 12, kRawFull = 14, kRawEmpty = 16, kHFull = 18, kXFull, kUDone, kDrain, kZFull, kZEmpty, kTold, kBars = kTold + 4
 };
 
 // What a block works on.
@@ -634,6 +634,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         }
         mbar_init(bar(kXFull), 16);
         mbar_init(bar(kHFull), 16);
+        for (int i = 0; i < 4; ++i)
+            mbar_init(bar(kTold + i), 4);
         mbar_init(bar(kUDone), 1);
         mbar_init(bar(kDrain), 1);
         for (int i = 0; i < 2; ++i) {
@@ -1037,7 +1039,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 }
             }
         };
-        // The four warps of the same rows meet: what each told is there for the others.
+        // The four warps of the same rows meet: what each told is there for the others.  In the loops they arrive when
+        // they have told it and wait when they need it (with a meeting there the output pass took 147 us for 144.6).
         auto meet = [&]() { __syncwarp(); asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); };
         auto told_by_all = [&]() { return *reinterpret_cast<const uint2 *>(told[row]); };
         // x' = x w
@@ -1094,12 +1097,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                 f2 xw[8];
                 weigh(x, wt, xw);
                 reinterpret_cast<uint8_t *>(told[row])[4 * (c & 1) + part] = (uint8_t)exponent(largest(xw));
+                arrive(kTold + q);
                 if (c >= 2) {
                     ok = ok && i_done(c - 2);
                     tc_fence_after();
                     add_acc(1, r1, K::kDH + (c & 1) * 128);
                 }
-                meet();
+                ok = ok && wait_all(kTold + q, c & 1);
                 const uint32_t t = reinterpret_cast<const uint32_t *>(told[row])[c & 1];
                 const int e = largest_half(t & 0x00ff00ffu, (t >> 8) & 0x00ff00ffu);
                 put(std::true_type(), xw, up(e), c & 1 ? K::kX : K::kXP);
@@ -1204,8 +1208,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     ok = ok && wait_all(kUDone, c & 1);
                     tc_fence_after();
                 }
-                if (more) // (all four have read what was told before, or U would not be done)
+                if (more) { // (all four have read what was told before, or U would not be done)
                     told[row][part] = (uint16_t)mine;
+                    arrive(kTold + q);
+                }
                 if (c >= 0) {
                     if constexpr (kWhole<T>)
                         add_acc(step, 1, K::kDH);
@@ -1225,7 +1231,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                         tmem_st8(tmem + lanes + K::kDH + CW * part + i / 2, hi);
                         tmem_st8(tmem + lanes + K::kDH + CW * part + CW / 2 + i / 2, lo);
                     }
-                    meet();
+                    ok = ok && wait_all(kTold + q, (c + 1) & 1);
                     const uint2 t = told_by_all();
                     const int ew = largest_half(t.x, t.y) >> 8;
                     then = mine & 0xff000000u;
