@@ -614,7 +614,8 @@ def ssm_prefill(cfg: SsmConfig, xbc, dt, cu_seqlens, conv_w, A_log, *, conv_b=No
     xbc [N, H P + 2 G S], dt [N, H] and z [N, H, P] may be slices of wider rows.  Returns a dict
     with "y" [N, H, P] and, when requested or passed in, "final_state" [B, H, P, S] float32 and
     "final_conv" [B, 3, H P + 2 G S]; ``final_state`` may be ``initial_state``, and ``final_conv``
-    ``initial_conv``."""
+    ``initial_conv``.  The state keeps float32's precision (some 1e-7), and so does a float32 y;
+    a bfloat16 y is read out to 2^-17 before its rounding."""
     import torch
     N, B, dev, act = xbc.shape[0], cu_seqlens.shape[0] - 1, xbc.device, _act(cfg)
     H, P, S, C = cfg.num_heads, cfg.head_dim, cfg.state_dim, cfg.conv_dim

@@ -273,7 +273,8 @@ constexpr size_t kWideSmem = 1024 + (size_t)kWideStages * (128 + kWideN) * kBK;
 // to 64 register sums while the tensor core works on the next one in the other
 // half of TMEM.  Reading TMEM is latency that only other warps hide: two
 // warpgroups of 128 columns took 146 us at 4096 x 12352 x 2048, four take 128.
-// 4096 x 8192 x 16384: 500 us, 2190 TFLOP/s; what bounds it is this reading and
+// 4096 x 8192 x 16384: 500 us, 2190 TFLOP/s, in short runs, 600 us and 1830 TFLOP/s
+// called back to back, at the power limit; what bounds it is this reading and
 // adding, 32768 values for each 128 x 256 x 128 products.
 template <typename O>
 __global__ void __launch_bounds__(kWideThreads, 1)

@@ -18,7 +18,7 @@
 // With few sequences each is cut into segments, and a first run of the scan
 // kernel, without outputs, finds what each segment adds to the state.
 //
-// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 210 us (by
+// 4096 tokens of 128 heads of 64, 8 groups, 128 states, bfloat16: 208 us (by
 // themselves: prep 31, summary 42, output pass 145), where moving the bytes would
 // take 35 and the MMAs 50.  What bounds it is the 16 warps' instructions and their
 // latency: two thirds of the issue slots, four such warps to a scheduler (the

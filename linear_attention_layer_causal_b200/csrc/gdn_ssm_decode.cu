@@ -9,7 +9,8 @@
 // A block takes units of 64 state rows of one group.  Its first unit's states
 // are requested before the convolution, whose latency they cover, and each
 // later unit's before the unit ahead of it is worked on.  256 sequences of 128
-// heads of 64 and 128 states: 337 us, 6.5 TB/s; one sequence 5.2 us.
+// heads of 64 and 128 states: 337 us, 6.5 TB/s; one sequence 5.2 us, in two kernels
+// (the windows of B and C move on behind the blocks that read them).
 #include "gdn_ssm.cuh"
 
 namespace gdn {
