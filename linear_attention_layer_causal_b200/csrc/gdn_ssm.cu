@@ -887,8 +887,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                     Ds[h] = D[h];
                 }
                 if (kWhole<T>) {
-                    // the largest C . B times the largest delta, of which no mask is above 1, brought to 2^15 at most; D, which
-                    // is to be added to it, may ask for less
+                    // the largest C . B times the largest delta, of which no mask is above 1, brought below 2^14; D, which is
+                    // to be added to it, may ask for less, to be below that too
                     const uint8_t *factors = sm + K::kOffCb + cs * K::kCbBytes + 64; // (row 0, column 16)
                     const int bc = 254 - exponent(*reinterpret_cast<const float *>(factors)) - exponent(*reinterpret_cast<const float *>(factors + 4));
 #pragma unroll
@@ -899,8 +899,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
                             const uint32_t v = __float_as_uint(mask[cs][h][128 + 2 * lane + k]) & 0x7fffffffu;
                             most = max(most, v < 0x7f800000u ? v : 0u);
                         }
-                        const int m = 267 - exponent(*reinterpret_cast<const float *>(factors + 8)) - (int)(__reduce_max_sync(0xffffffffu, most) >> 23);
-                        const int n = max(min(min(bc + m, 141 - exponent(D[h])), 126), -126);
+                        const int m = 266 - exponent(*reinterpret_cast<const float *>(factors + 8)) - (int)(__reduce_max_sync(0xffffffffu, most) >> 23);
+                        const int n = max(min(min(bc + m, 140 - exponent(D[h])), 126), -126);
                         fm[h] = pow2(n - bc);
                         Ds[h] = D[h] * pow2(n);
                         if (warp == 2 && lane == 0)

@@ -180,3 +180,25 @@ def test_long_memory():
     d["dt"] = torch.full_like(d["dt"], -9.2)
     d["dt_bias"] = None
     check(cfg, d, [5000], norm=False)
+
+
+@pytest.mark.gpu
+def test_masks_and_skip_at_the_top_of_their_range():
+    """C . B, the step and D all just below a power of two, so that each takes the most of what its scale allows and
+    their sum twice that: still finite, and exact."""
+    cfg = gdn.SsmConfig(1, 1, 64, 64, act_dtype="f32", dt_min=1.4426948, dt_max=1.4426948)  # times ln 2: 1 - 2^-22
+    d, cu = make(cfg, [64], 68, gate=False, init=False, extras=False)
+    top = 2.0 - 2.0 ** -20
+    d["conv_w"].zero_()
+    d["conv_w"][:, 3] = 1
+    x = torch.linspace(1.0, 3.0, 4001, dtype=torch.float64)
+    silu = x * torch.sigmoid(x)
+    b = float(x[(silu - 1).abs().argmin()])  # SiLU(b) next to 1: 64 columns of 1 are 64, their neighbours below
+    for shift in (-1e-3, -1e-4, 0.0, 1e-4, 1e-3):
+        d["xbc"][:, 64:] = b + shift
+        for D in (top, -top, 1.0, top * 2.0 ** -3, top * 2.0 ** 7):
+            d["D"] = torch.full((1,), D, device="cuda")
+            out = prefill(cfg, d, cu, return_final_state=True)
+            e = want(cfg, d, [64])
+            near(out["y"], e["y"], e["y_mag"], "y", False)
+            near(out["final_state"], e["state"], e["state_mag"], "state", False)
